@@ -8,6 +8,14 @@ does all the work; this package only marshals arguments and sequences the
 per-cell calls of a looped decode step.
 """
 
+from .chunk import (  # noqa: F401
+    Rotary,
+    loopkv_chunk_attention,
+    loopkv_norm_rope,
+    loopkv_read_tokens,
+    loopkv_rope_append,
+    rope_table,
+)
 from .loopkv import (  # noqa: F401
     KIND_CODES,
     LIB_PATH,
