@@ -1,0 +1,745 @@
+// Chunk attention on the tensor cores (sm_100a): the kernel of chunk_attention.cu.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "chunk_common.cuh"
+#include "tcgen05.cuh"
+
+namespace loopkv {
+
+constexpr int kTileKeys = 128;                       // keys of one tile: eight blocks
+constexpr int kDequantWarps = kTileKeys / kBlock;    // one block each
+constexpr int kExpRing = 4;
+
+// A block's keys (values) are stored as x 2^-e with e such that the largest is
+// in [2^-7, 2^-6): then 2^24 times a 4-bit scale, at most 2^24 (2 2^-6 / 15)
+// (1 + 2^-8) < 35200, is a finite fp16 number, and the code itself, read as a
+// subnormal fp16 number (code 2^-24), needs no conversion.
+constexpr int kTopExp = -6;
+
+template <int D, int MT>
+struct ChunkSmem {
+  static constexpr int kTile = kTileKeys * D * 2;    // one K or V stage, one Q tile
+  static constexpr int kQ = 0;
+  static constexpr int kK = MT * kTile;
+  static constexpr int kV = kK + 2 * kTile;
+  static constexpr int kMeta = kV + 2 * kTile;       // per dequantising warp: key scales and minima, fp16
+  static constexpr int kKExp = kMeta + kDequantWarps * D * 4;
+  static constexpr int kVExp = kKExp + kExpRing * kDequantWarps * 4;
+  static constexpr int kStats = kVExp + kExpRing * kDequantWarps * 4;   // (max, sum) of each row
+  static constexpr int kBars = kStats + MT * 128 * 8;
+  static constexpr int kBarCount = 8 + 3 * 2;
+  static constexpr int kTmem = kBars + kBarCount * 8;
+  static constexpr int kFlags = kTmem + 4;           // value exponent of O, fault bits
+  static constexpr int kBytes = kFlags + 12;
+  static constexpr int kPartial = kK;                // fp32 partial O over the stages: MT 128 D 4 = MT kTile 2 <= 4 kTile
+};
+
+template <int D, int MT>
+__host__ __device__ constexpr int chunk_threads() { return (MT * 4 + kDequantWarps + 1) * 32; }
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// 2^e as a float, e in [-149, 127].
+__device__ __forceinline__ float pow2f(int e) {
+  return e >= -126 ? __int_as_float((e + 127) << 23) : __int_as_float(1 << (e + 149));
+}
+
+// Exponent e of a block whose largest absolute value has the float bits u:
+// the value times 2^-e is in [2^-7, 2^-6) (smaller where e is held at -100).
+__device__ __forceinline__ int block_exp(uint32_t abs_bits) {
+  return max(static_cast<int>(abs_bits >> 23) - 127 - kTopExp + 1, -100);
+}
+
+// 16 channels' codes (hi << 2 | lo, two bits each plane; 2-bit cells: code << 2)
+// as fp16 x = code s + m: eight half2 words of neighbouring channels.  s, m:
+// scale and minimum of each channel pair; the scale of a pair is 2^24 or 2^20
+// times its value by the place that its codes have in a word.
+template <bool SPLIT, typename S, typename M>
+__device__ __forceinline__ void codes_to_half(uint32_t hi, uint32_t lo, S&& s, M&& m, uint32_t (&out)[8]) {
+  uint32_t even, odd;  // nibble n: channel 2 n, 2 n + 1
+  if constexpr (SPLIT) {
+    even = ((hi << 2) & 0xCCCCCCCCu) | (lo & 0x33333333u);
+    odd = (hi & 0xCCCCCCCCu) | ((lo >> 2) & 0x33333333u);
+  } else {
+    even = (hi << 2) & 0xCCCCCCCCu;
+    odd = hi & 0xCCCCCCCCu;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {  // channels 0-7, 8-15
+    uint32_t x = __byte_perm(even, odd, j ? 0x7632 : 0x5410);
+#pragma unroll
+    for (int n = 0; n < 4; n += 2) {
+      out[4 * j + n] = half2_bits(__hfma2(bits_half2(x & 0x000F000Fu), s(4 * j + n), m(4 * j + n)));
+      out[4 * j + n + 1] = half2_bits(__hfma2(bits_half2(x & 0x00F000F0u), s(4 * j + n + 1), m(4 * j + n + 1)));
+      x >>= 8;
+    }
+  }
+}
+
+// Byte offset of the 16-byte chunk of channels 8 c .. 8 c + 7 of row r in a
+// swizzled tile of 128-byte rows (64 channels a row, 128 rows a sub-tile).
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return (c >> 3) * (kTileKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+
+// bf16 pair times f (a power of two) as fp16 pair.
+__device__ __forceinline__ uint32_t bf16x2_to_half(uint32_t w, float f) {
+  return half2_bits(__floats2half2_rn(bf16_lo(w) * f, bf16_hi(w) * f));
+}
+
+// Bounded wait of a whole warp; the same answer for all its threads.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// What the CTA works on.
+struct ChunkJob {
+  int b, hk, start, len;      // sequence, KV head, its chunk
+  int stored;                 // tokens in the cell that its rows may see
+  int stored_tiles;           // tiles over them; the chunk's own rows (exact) come after
+  int tile0, tiles;           // this CTA's tiles
+  bool current;
+};
+
+// ---------------------------------------------------------------- dequantising warps
+
+// One block of 16 tokens: 16 channels a thread, KPL tokens a thread.
+template <int KIND, int D>
+struct BlockLoader {
+  using R = Rec<KIND, D>;
+  static constexpr int C16 = D / 16, SUBS = 32 / C16, KPL = kBlock / SUBS;
+  static constexpr bool kQuant = KIND != LOOPKV_CELL_BF16;
+  static constexpr bool kSplit = KIND == LOOPKV_CELL_Q4;
+
+  struct Raw {  // of one block, as loaded
+    uint32_t khi[KPL], klo[KPL], vhi[4], vlo[KPL], vmeta[KPL];
+    uint32_t kmeta[D / 32];
+  };
+
+  const ChunkAttnParams& p;
+  const ChunkJob& job;
+  int block, lane, c16, sub;
+
+  __device__ BlockLoader(const ChunkAttnParams& p, const ChunkJob& job, int block, int lane)
+      : p(p), job(job), block(block), lane(lane), c16(lane % C16), sub(lane / C16) {}
+
+  // The thread's tokens.  Where eight neighbouring threads would write rows of
+  // the same parity to the same banks, half of them take the other row first.
+  __device__ int key_token(int it) const { return it * SUBS + (D == 128 ? sub ^ (c16 >> 2) : sub); }
+  __device__ int value_token(int k) const { return sub * KPL + (k ^ (D == 128 ? c16 >> 2 : sub & 1)); }
+
+  __device__ int token0(int tile) const { return tile * kTileKeys + block * kBlock; }
+  // the key group of the block is full, so its keys are quantised
+  __device__ bool full(int t0) const { return (t0 & ~(kGroup - 1)) + kGroup <= job.stored; }
+
+  // Physical ids of this warp's block and of its group's other one (all ids of
+  // the sequence's stored blocks were checked); 0 where there is none.
+  __device__ int2 ids(int tile) const {
+    const int t0 = token0(tile);
+    if (tile >= job.stored_tiles || t0 >= job.stored) return make_int2(0, 0);
+    const int32_t* row = p.block_table + static_cast<size_t>(job.b) * p.max_blocks;
+    return make_int2(row[t0 / kBlock], full(t0) ? row[(t0 ^ kBlock) / kBlock] : 0);
+  }
+
+  __device__ const uint8_t* record(int phys) const {
+    return p.arena + (static_cast<size_t>(phys) * p.Hkv + job.hk) * R::kBytes;
+  }
+
+  __device__ void load(int tile, int2 id, Raw& r) const {
+    const int t0 = token0(tile);
+    if (!kQuant || tile >= job.stored_tiles || t0 >= job.stored) return;
+    const uint8_t* rec = record(id.x);
+    if (full(t0)) {
+      const uint8_t* other = record(id.y);
+      // this thread's D / 32 channels of the group's scales
+      const int ch = lane * (D / 32);
+      const uint8_t* mrec = ((ch >= D / 2) == ((t0 & kBlock) != 0) ? rec : other) + R::kKMetaOff + (ch % (D / 2)) * 4;
+      if constexpr (D == 128) {
+        const uint4 w = *reinterpret_cast<const uint4*>(mrec);
+        r.kmeta[0] = w.x, r.kmeta[1] = w.y, r.kmeta[2] = w.z, r.kmeta[3] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(mrec);
+        r.kmeta[0] = w.x, r.kmeta[1] = w.y;
+      }
+#pragma unroll
+      for (int it = 0; it < KPL; ++it) {
+        const int at = key_token(it) * R::kRow + 4 * c16;
+        r.khi[it] = *reinterpret_cast<const uint32_t*>(rec + R::kKHi + at);
+        if constexpr (kSplit) r.klo[it] = *reinterpret_cast<const uint32_t*>(rec + R::kQ4KLo + at);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint8_t* col = rec + R::kVHi + (4 * c16 + q) * kBlock + sub * KPL;
+      r.vhi[q] = KPL == 4 ? *reinterpret_cast<const uint32_t*>(col) : *reinterpret_cast<const uint16_t*>(col);
+    }
+#pragma unroll
+    for (int k = 0; k < KPL; ++k) {
+      const int t = value_token(k);
+      if constexpr (kSplit) r.vlo[k] = *reinterpret_cast<const uint32_t*>(rec + R::kQ4VLo + t * R::kRow + 4 * c16);
+      r.vmeta[k] = *reinterpret_cast<const uint32_t*>(rec + R::kVMetaOff + (t * (D / kGroup) + c16 / 2) * 4);
+    }
+  }
+
+  __device__ void store_row(uint32_t tile_base, int token, const uint32_t (&x)[8]) const {
+    const int r = block * kBlock + token;
+    st_shared16(tile_base + swz(r, 2 * c16), x[0], x[1], x[2], x[3]);
+    st_shared16(tile_base + swz(r, 2 * c16 + 1), x[4], x[5], x[6], x[7]);
+  }
+
+  // Exact bf16 rows into the tile; row(token) is the token's row or null (zeros).
+  template <bool KEYS, typename Row>
+  __device__ int store_exact(uint32_t tile_base, Row&& row) const {
+    uint4 w[KPL][2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < KPL; ++k) {
+      const __nv_bfloat16* src = row(KEYS ? key_token(k) : value_token(k));
+      w[k][0] = w[k][1] = make_uint4(0, 0, 0, 0);
+      if (src) {
+        w[k][0] = reinterpret_cast<const uint4*>(src + 16 * c16)[0];
+        w[k][1] = reinterpret_cast<const uint4*>(src + 16 * c16)[1];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KPL; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        top = abs_max_bf16x2(abs_max_bf16x2(top, w[k][j].x), w[k][j].y);
+        top = abs_max_bf16x2(abs_max_bf16x2(top, w[k][j].z), w[k][j].w);
+      }
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    const int e = block_exp(top << 16);
+    const float f = pow2f(-e);
+#pragma unroll
+    for (int k = 0; k < KPL; ++k) {
+      uint32_t x[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[4 * j] = bf16x2_to_half(w[k][j].x, f), x[4 * j + 1] = bf16x2_to_half(w[k][j].y, f);
+        x[4 * j + 2] = bf16x2_to_half(w[k][j].z, f), x[4 * j + 3] = bf16x2_to_half(w[k][j].w, f);
+      }
+      store_row(tile_base, KEYS ? key_token(k) : value_token(k), x);
+    }
+    return e;
+  }
+
+  // Keys of the block; returns their exponent.
+  __device__ int store_keys(int tile, int2 id, const Raw& r, uint32_t tile_base, uint32_t meta) const {
+    const int t0 = token0(tile);
+    if (tile >= job.stored_tiles) {
+      const int c0 = t0 - job.stored_tiles * kTileKeys;
+      return store_exact<true>(tile_base, [&](int t) {
+        return c0 + t < job.len ? row_at(p.k_cur, job.b, c0 + t, job.hk) : nullptr;
+      });
+    }
+    if constexpr (kQuant) {
+      if (!full(t0)) {
+        const __nv_bfloat16* res = p.residual + (static_cast<size_t>(job.b) * p.Hkv + job.hk) * kGroup * D;
+        return store_exact<true>(tile_base, [&](int t) {
+          return t0 + t < job.stored ? res + ((t0 + t) % kGroup) * D : nullptr;
+        });
+      }
+      // scales and minima of the group's channels, fp16, shared by the warp
+      constexpr int CPT = D / 32;
+      constexpr float kTop = kSplit ? 15.f : 3.f;
+      float s[CPT], mn[CPT], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        s[i] = bf16_lo(r.kmeta[i]), mn[i] = bf16_hi(r.kmeta[i]);
+        top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(s[i], kTop, mn[i]))));
+      }
+      const int e = block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      const float f = pow2f(-e), fs = f * (kSplit ? 0x1p24f : 0x1p22f);
+      // pair n of eight channels: 2^24 for even n, 2^20 for odd; parts of 16 bytes
+      // [scale 0-7][scale 8-15][min 0-7][min 8-15] x C16 so that reads do not collide
+#pragma unroll
+      for (int i = 0; i < CPT; i += 2) {
+        const int ch = lane * CPT + i, pair = (ch / 2) % 4;
+        const float g = pair & 1 ? fs * 0.0625f : fs;
+        const uint32_t at = meta + ((ch % 16) / 8 * C16 + ch / 16) * 16 + pair * 4;
+        const uint32_t hs = half2_bits(__floats2half2_rn(s[i] * g, s[i + 1] * g));
+        const uint32_t hm = half2_bits(__floats2half2_rn(mn[i] * f, mn[i + 1] * f));
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hs) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 2 * C16 * 16), "r"(hm) : "memory");
+      }
+      __syncwarp();
+      uint32_t sw[8], mw[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(sw[4 * j]), "=r"(sw[4 * j + 1]), "=r"(sw[4 * j + 2]), "=r"(sw[4 * j + 3])
+                     : "r"(meta + (j * C16 + c16) * 16) : "memory");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(mw[4 * j]), "=r"(mw[4 * j + 1]), "=r"(mw[4 * j + 2]), "=r"(mw[4 * j + 3])
+                     : "r"(meta + ((2 + j) * C16 + c16) * 16) : "memory");
+      }
+      __syncwarp();
+#pragma unroll
+      for (int it = 0; it < KPL; ++it) {
+        uint32_t x[8];
+        codes_to_half<kSplit>(r.khi[it], kSplit ? r.klo[it] : 0u, [&](int n) { return bits_half2(sw[n]); },
+                              [&](int n) { return bits_half2(mw[n]); }, x);
+        store_row(tile_base, key_token(it), x);
+      }
+      return e;
+    } else {
+      const uint8_t* rec = record(id.x);
+      return store_exact<true>(tile_base, [&](int t) {
+        return t0 + t < job.stored ? reinterpret_cast<const __nv_bfloat16*>(rec + R::kBfK) + t * D : nullptr;
+      });
+    }
+  }
+
+  // Values of the block; returns their exponent.
+  __device__ int store_values(int tile, int2 id, const Raw& r, uint32_t tile_base) const {
+    const int t0 = token0(tile);
+    if (tile >= job.stored_tiles) {
+      const int c0 = t0 - job.stored_tiles * kTileKeys;
+      return store_exact<false>(tile_base, [&](int t) {
+        return c0 + t < job.len ? row_at(p.v_cur, job.b, c0 + t, job.hk) : nullptr;
+      });
+    }
+    if constexpr (kQuant) {
+      constexpr float kTop = kSplit ? 15.f : 3.f;
+      float s[KPL], mn[KPL], top = 0.f;
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) {
+        // what lies behind the last token is no value
+        const uint32_t w = t0 + value_token(k) < job.stored ? r.vmeta[k] : 0u;
+        s[k] = bf16_lo(w), mn[k] = bf16_hi(w);
+        top = fmaxf(top, fmaxf(fabsf(mn[k]), fabsf(fmaf(s[k], kTop, mn[k]))));
+      }
+      const int e = block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      const float f = pow2f(-e), fs = f * (kSplit ? 0x1p24f : 0x1p22f);
+#pragma unroll
+      for (int k = 0; k < KPL; ++k) {
+        const int b = D == 128 ? k ^ (c16 >> 2) : k ^ (sub & 1);  // byte of the token in the column words
+        const uint32_t sel = b | ((4 + b) << 4);
+        const uint32_t hi = __byte_perm(__byte_perm(r.vhi[0], r.vhi[1], sel), __byte_perm(r.vhi[2], r.vhi[3], sel), 0x5410);
+        const __half2 sa = __float2half2_rn(s[k] * fs), sb = __float2half2_rn(s[k] * (fs * 0.0625f));
+        const __half2 m = __float2half2_rn(mn[k] * f);
+        uint32_t x[8];
+        codes_to_half<kSplit>(hi, kSplit ? r.vlo[k] : 0u, [&](int n) { return n & 1 ? sb : sa; }, [&](int) { return m; }, x);
+        store_row(tile_base, value_token(k), x);
+      }
+      return e;
+    } else {
+      const uint8_t* rec = record(id.x);
+      return store_exact<false>(tile_base, [&](int t) {
+        return t0 + t < job.stored ? reinterpret_cast<const __nv_bfloat16*>(rec + R::kBfV) + t * D : nullptr;
+      });
+    }
+  }
+};
+
+// ---------------------------------------------------------------- the kernel
+
+template <int KIND, int D, int MT>
+__global__ void __launch_bounds__(chunk_threads<D, MT>(), 1) chunk_tensor_kernel(const ChunkAttnParams p, int row_tiles,
+                                                                               int splits) {
+  using L = ChunkSmem<D, MT>;
+  constexpr int kThreads = chunk_threads<D, MT>(), kRows = MT * 128;
+  constexpr int kTmemCols = MT * (kTileKeys + D) <= 256 ? 256 : 512;
+  constexpr int kSoftmaxWarps = MT * 4;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % splits;
+  const uint32_t unit = blockIdx.x / splits;
+  const int tile = row_tiles - 1 - static_cast<int>(unit % row_tiles);  // the rows that see most come first
+
+  ChunkJob job;
+  job.hk = (unit / row_tiles) % p.Hkv;
+  job.b = unit / row_tiles / p.Hkv;
+  job.current = p.k_cur.p != nullptr;
+  job.start = p.chunk.start_pos[job.b];
+  job.len = p.chunk.new_lens ? p.chunk.new_lens[job.b] : p.chunk.T;
+  const bool first_cta = tile == 0 && job.hk == 0 && rank == 0;
+  if (job.len < 0 || job.len > p.chunk.T) {
+    if (first_cta && threadIdx.x == 0 && job.start >= 0) flag_error(p.chunk.err, LOOPKV_DEVERR_SEQ_LEN);
+    return;
+  }
+  const int rows = job.len << p.g_log2, row0 = tile * kRows;
+  if (row0 >= rows) return;
+  const int row_end = min(rows, row0 + kRows), last_token = (row_end - 1) >> p.g_log2;
+  const int64_t stored64 = static_cast<int64_t>(job.start) + (job.current ? 0 : job.len);
+  bool zero = job.start < 0;
+  int fault = 0;
+  if (!zero && stored64 > p.max_stored) {
+    fault = LOOPKV_DEVERR_SEQ_LEN;
+    zero = true;
+  }
+  job.stored = zero ? 0 : static_cast<int>(stored64);
+  if (!zero) {
+    // every block of the sequence, so that all its rows are answered alike
+    const int blocks = (job.stored + kBlock - 1) / kBlock;
+    int bad = 0;
+    for (int i = threadIdx.x; i < blocks; i += kThreads) {
+      const int phys = p.block_table[static_cast<size_t>(job.b) * p.max_blocks + i];
+      bad |= phys < 0 || phys >= p.num_blocks;
+    }
+    if (__syncthreads_or(bad)) {
+      fault = LOOPKV_DEVERR_BLOCK_ID;
+      zero = true;
+    }
+  }
+  const int G = 1 << p.g_log2;
+  // this thread's row (softmax warps): row m * 128 + lane of the tile
+  const int my_row = min(row0 + threadIdx.x, row_end - 1);
+  if (zero) {
+    if (fault && threadIdx.x == 0) flag_error(p.chunk.err, fault);
+    if (rank == 0)
+      for (int i = threadIdx.x; i < (row_end - row0) * (D / 8); i += kThreads) {
+        const int r = row0 + i / (D / 8);
+        __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + (r >> p.g_log2)) * p.H +
+                                    (job.hk << p.g_log2) + (r & (G - 1))) * D;
+        reinterpret_cast<uint4*>(o)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+      }
+    return;
+  }
+  // keys that the tile's last row sees, 128 at a time; this CTA's share of them
+  const int seen = job.current ? job.stored : min(job.stored, job.start + last_token + 1);
+  job.stored_tiles = (seen + kTileKeys - 1) / kTileKeys;
+  const int all_tiles = job.stored_tiles + (job.current ? last_token / kTileKeys + 1 : 0);
+  job.tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * rank / splits);
+  job.tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (rank + 1) / splits) - job.tile0;
+
+  const uint32_t bars = sbase + L::kBars;
+  auto k_full = [&](int s) { return bars + 8 * s; };
+  auto k_empty = [&](int s) { return bars + 16 + 8 * s; };
+  auto v_full = [&](int s) { return bars + 32 + 8 * s; };
+  auto v_empty = [&](int s) { return bars + 48 + 8 * s; };
+  auto s_full = [&](int m) { return bars + 64 + 8 * m; };
+  auto p_full = [&](int m) { return bars + 80 + 8 * m; };
+  auto o_done = [&](int m) { return bars + 96 + 8 * m; };
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlags);  // [0]: O's value exponent, [1]: a wait gave up
+  float* k_exp = reinterpret_cast<float*>(smem + L::kKExp);
+  int* v_exp = reinterpret_cast<int*>(smem + L::kVExp);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(k_full(s), kDequantWarps);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), kDequantWarps);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(s_full(m), 1);
+      mbar_init(p_full(m), 4);
+      mbar_init(o_done(m), 1);
+    }
+    fence_mbar_init();
+    flags[1] = 0;
+  }
+  if (warp == kSoftmaxWarps + kDequantWarps) tmem_alloc<kTmemCols>(sbase + L::kTmem);
+
+  // Queries: a row a thread, times a power of two that brings its largest entry
+  // to [2^13, 2^14) (bf16's 8 bits stay whole in fp16), sign of the scale with it.
+  float row_scale = 0.f;
+  if (warp < kSoftmaxWarps) {
+    const uint4* src = reinterpret_cast<const uint4*>(
+        row_at(p.q, job.b, my_row >> p.g_log2, (job.hk << p.g_log2) + (my_row & (G - 1))));
+    uint4 w[D / 8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) w[i] = src[i];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      top = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(top, w[i].x), w[i].y), w[i].z), w[i].w);
+    const int e = max(static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127 - 13, -100);
+    const float f = p.sm_scale_log2 < 0.f ? -pow2f(-e) : pow2f(-e);
+    row_scale = fabsf(p.sm_scale_log2) * pow2f(e);
+    const uint32_t q = sbase + L::kQ + (warp / 4) * L::kTile;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      st_shared16(q + swz(threadIdx.x % 128, i), bf16x2_to_half(w[i].x, f), bf16x2_to_half(w[i].y, f),
+                  bf16x2_to_half(w[i].z, f), bf16x2_to_half(w[i].w, f));
+    fence_proxy_async_shared();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmem);
+  const uint32_t tmem_o = tmem + MT * kTileKeys;
+  bool ok = true;
+  const int n = job.tiles;
+
+  if (warp >= kSoftmaxWarps && warp < kSoftmaxWarps + kDequantWarps) {
+    // ------------------------------------------------------------ dequantise
+    const int block = warp - kSoftmaxWarps;
+    const BlockLoader<KIND, D> loader(p, job, block, lane);
+    typename BlockLoader<KIND, D>::Raw cur, next;
+    // the ids two tiles ahead, the records one
+    int2 id = n > 0 ? loader.ids(job.tile0) : make_int2(0, 0), id_next = n > 1 ? loader.ids(job.tile0 + 1) : id;
+    if (n > 0) loader.load(job.tile0, id, cur);
+    for (int j = 0; j < n && ok; ++j) {
+      const int s = j & 1, ring = j % kExpRing;
+      if (j + 1 < n) loader.load(job.tile0 + j + 1, id_next, next);
+      const int2 id_after = j + 2 < n ? loader.ids(job.tile0 + j + 2) : id_next;
+      if (j >= 2) ok = warp_wait(k_empty(s), ((j >> 1) - 1) & 1);
+      if (!ok) break;
+      const int ke = loader.store_keys(job.tile0 + j, id, cur, sbase + L::kK + s * L::kTile, sbase + L::kMeta + block * D * 4);
+      if (lane == 0) k_exp[ring * kDequantWarps + block] = pow2f(max(min(ke, 127), -149));
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full(s));
+      if (j >= 2) ok = warp_wait(v_empty(s), ((j >> 1) - 1) & 1);
+      if (!ok) break;
+      const int ve = loader.store_values(job.tile0 + j, id, cur, sbase + L::kV + s * L::kTile);
+      if (lane == 0) v_exp[ring * kDequantWarps + block] = ve;
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full(s));
+      cur = next;
+      id = id_next;
+      id_next = id_after;
+    }
+  } else if (warp == kSoftmaxWarps + kDequantWarps) {
+    // ------------------------------------------------------------ multiply
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t kQKDesc = f16_idesc(kTileKeys, false), kPVDesc = f16_idesc(D, true);
+      auto issue_qk = [&](int m, int s) {
+        const uint32_t q = sbase + L::kQ + m * L::kTile, k = sbase + L::kK + s * L::kTile;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t at = (i / 4) * (kTileKeys * 128) + (i % 4) * 32;
+          mma_ss(tmem + m * kTileKeys, smem_desc(q + at, 16), smem_desc(k + at, 16), kQKDesc, i > 0);
+        }
+        mma_commit(s_full(m));
+      };
+      ok = mbar_wait(k_full(0), 0);
+      tc_fence_after();
+      if (ok) {
+        for (int m = 0; m < MT; ++m) issue_qk(m, 0);
+        mma_commit(k_empty(0));
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int s = j & 1;
+        ok = mbar_wait(v_full(s), (j >> 1) & 1);
+        for (int m = 0; m < MT && ok; ++m) {
+          ok = mbar_wait(p_full(m), j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v = sbase + L::kV + s * L::kTile;
+#pragma unroll
+          for (int i = 0; i < kTileKeys / 16; ++i)
+            mma_ts(tmem_o + m * D, tmem + m * kTileKeys + i * 8, smem_desc(v + i * 2048, kTileKeys * 128), kPVDesc,
+                   j > 0 || i > 0);
+          mma_commit(o_done(m));
+          if (m == MT - 1) mma_commit(v_empty(s));
+          if (j + 1 < n) {
+            // the next logits take the columns of these weights
+            const int s1 = (j + 1) & 1;
+            if (m == 0) ok = mbar_wait(k_full(s1), ((j + 1) >> 1) & 1);
+            ok = ok && mbar_wait(o_done(m), j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_qk(m, s1);
+            if (m == MT - 1) mma_commit(k_empty(s1));
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int m = warp / 4;
+    const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // tensor-memory lanes 32 (warp % 4) on
+    const uint32_t ts = tmem + m * kTileKeys + lanes, to = tmem_o + m * D + lanes;
+    const bool idle = row0 + warp * 32 >= row_end;                 // no row of this warp is there
+    const int token = my_row >> p.g_log2;
+    float m_ref = -INFINITY, sum = 0.f;
+    int v_ref = -1000;
+    for (int j = 0; j < n && ok; ++j) {
+      const int gt = job.tile0 + j, ring = j % kExpRing;
+      ok = warp_wait(s_full(m), j & 1) && warp_wait(v_full(j & 1), (j >> 1) & 1);
+      if (!ok) break;
+      if (!idle) {
+        tc_fence_after();
+        // keys of this tile that the row sees
+        const int lim = gt >= job.stored_tiles ? token + 1 - (gt - job.stored_tiles) * kTileKeys
+                        : (job.current ? job.stored : job.start + token + 1) - gt * kTileKeys;
+        const bool masked = __any_sync(0xffffffffu, lim < kTileKeys);
+        const float* ke = k_exp + ring * kDequantWarps;
+        const int* ve = v_exp + ring * kDequantWarps;
+        float top = -INFINITY;
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(ts + 32 * c, r);
+          tmem_wait_ld();
+          float a = -INFINITY, b = -INFINITY;
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= lim) r[i] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) a = fmaxf(a, __uint_as_float(r[i])), b = fmaxf(b, __uint_as_float(r[16 + i]));
+          // -inf times a scale of zero is no number: keep what is masked out of the product
+          if (a > -INFINITY) top = fmaxf(top, a * (row_scale * ke[2 * c]));
+          if (b > -INFINITY) top = fmaxf(top, b * (row_scale * ke[2 * c + 1]));
+        }
+        int e_top = ve[0];
+#pragma unroll
+        for (int i = 1; i < kDequantWarps; ++i) e_top = max(e_top, ve[i]);
+        // The reference maximum follows the running one only when that is 2^8
+        // above it, the value exponent when a block is 2^4 above: weights stay
+        // below 2^12, and O is rescaled rarely.
+        const float m_new = top > m_ref + 8.f ? top : m_ref;
+        const int v_new = e_top > v_ref + 4 ? e_top : v_ref;
+        if (__any_sync(0xffffffffu, m_new != m_ref) || v_new != v_ref) {
+          const float shrink = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+          sum *= shrink;
+          if (j > 0) {
+            ok = warp_wait(o_done(m), (j - 1) & 1);
+            tc_fence_after();
+            const float f = shrink * pow2f(max(v_ref - v_new, -149));
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              tmem_ld32(to + c, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+              tmem_st32(to + c, r);
+            }
+            tmem_wait_st();
+          }
+          m_ref = m_new;
+          v_ref = v_new;
+        }
+        const float base = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(ts + 32 * c, r);
+          tmem_wait_ld();
+          uint32_t w[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = row_scale * ke[2 * c + h];
+            const int de = max(ve[2 * c + h] - v_ref, -100);
+            const float off = static_cast<float>(de) - base;
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float x = fmaf(__uint_as_float(r[16 * h + i]), f, off), y = fmaf(__uint_as_float(r[16 * h + i + 1]), f, off);
+              if (masked) {
+                if (32 * c + 16 * h + i >= lim) x = -INFINITY;
+                if (32 * c + 16 * h + i + 1 >= lim) y = -INFINITY;
+              }
+              x = fast_exp2(x), y = fast_exp2(y);
+              part += x + y;
+              w[8 * h + i / 2] = half2_bits(__floats2half2_rn(x, y));
+            }
+            sum = fmaf(part, pow2f(-de), sum);
+          }
+          tmem_st16(ts + 16 * c, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(m));
+    }
+    // ------------------------------------------------------------ results
+    if (n > 0 && ok) ok = warp_wait(o_done(m), (n - 1) & 1);
+    tc_fence_after();
+    if (!ok) flags[1] = 1;
+    if (!idle) {
+      const float f = pow2f(max(min(v_ref, 127), -149)) * (splits == 1 ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
+      const bool valid = row0 + threadIdx.x < row_end;
+      const int local = threadIdx.x;
+      __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + token) * p.H + (job.hk << p.g_log2) +
+                                  (my_row & (G - 1))) * D;
+      if (splits > 1) reinterpret_cast<float2*>(smem + L::kStats)[local] = make_float2(m_ref, sum);
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t r[32];
+        if (n > 0) {
+          tmem_ld32(to + c, r);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0;
+        }
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = ok ? __uint_as_float(r[i]) * f : 0.f;
+        if (splits == 1) {
+          if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(o + c + i) =
+                  make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]), pack_bf16(x[i + 4], x[i + 5]),
+                             pack_bf16(x[i + 6], x[i + 7]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(smem + L::kPartial + local * D * 4 + ((((c + i) / 4) ^ (local & (D / 4 - 1))) << 4)) =
+                make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+      }
+    }
+  }
+  if (!ok && lane == 0) {
+    flags[1] = 1;
+    flag_error(p.chunk.err, LOOPKV_DEVERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftmaxWarps + kDequantWarps) tmem_free<kTmemCols>(tmem);
+  if (splits == 1) return;
+
+  // ---------------------------------------------------------------- join the splits
+  // Every CTA holds its partial rows (times their value exponent) and their
+  // (max, sum); row i is put together by CTA i % splits from all of them.
+  cluster_sync_all();
+  const uint32_t stats = sbase + L::kStats, partial = sbase + L::kPartial;
+  constexpr int kWarps = kThreads / 32, kQuads = D / 4, kRowsPerWarp = 32 / kQuads;
+  const int quad = lane % kQuads;
+  for (int i = warp * kRowsPerWarp + lane / kQuads; ; i += kWarps * kRowsPerWarp) {
+    const int row = i * splits + rank;
+    if (row0 + row >= row_end) break;
+    float m_all = -INFINITY;
+    for (int s = 0; s < splits; ++s) {
+      float pm;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pm) : "r"(peer_addr(stats + row * 8, s)));
+      m_all = fmaxf(m_all, pm);
+    }
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < splits; ++s) {
+      float pm, ps;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(pm), "=f"(ps) : "r"(peer_addr(stats + row * 8, s)));
+      if (pm == -INFINITY) continue;  // it saw no key
+      const float wgt = fast_exp2(pm - m_all);
+      float4 x;
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                   : "r"(peer_addr(partial + row * D * 4 + ((quad ^ (row & (kQuads - 1))) << 4), s)));
+      sum = fmaf(wgt, ps, sum);
+      acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
+      acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int r = row0 + row;
+    __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + (r >> p.g_log2)) * p.H +
+                                (job.hk << p.g_log2) + (r & (G - 1))) * D;
+    reinterpret_cast<uint2*>(o)[quad] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  }
+  cluster_sync_all();
+}
+
+}  // namespace loopkv
