@@ -64,116 +64,122 @@ class Rotary:
     """
 
     def __init__(self, table=None, interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6):
-        if table is not None:
-            _tensor(table, "table", torch.float32, 2)
-            if not table.is_contiguous():
-                raise ValueError("table must be contiguous")
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None:
-                _tensor(w, name, torch.bfloat16, 1)
-                if not w.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous")
+        parts = {"table": (table, torch.float32, 2), "q_weight": (q_weight, torch.bfloat16, 1),
+                 "k_weight": (k_weight, torch.bfloat16, 1)}
+        devices, self._dims = set(), {}
+        for name, (x, dtype, dims) in parts.items():
+            if x is None:
+                continue
+            if not isinstance(x, torch.Tensor) or not x.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if x.dtype != dtype or x.dim() != dims or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of {dims} dimensions")
+            devices.add(x.get_device())
+            if dims == 1:
+                self._dims[name] = int(x.shape[0])
+        if len(devices) > 1:
+            raise ValueError("the table and the weights are on different devices")
+        self._device = devices.pop() if devices else None
         self.table, self.q_weight, self.k_weight = table, q_weight, k_weight
         self.interleaved, self.eps = bool(interleaved), float(eps)
         positions, dim = (0, 0) if table is None else table.shape
         self.struct = loopkv_rotary(_data(table), int(positions), int(dim), int(self.interleaved), _data(q_weight),
                                     _data(k_weight), self.eps)
 
-    def _check(self, head_dim: int, device):
-        for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
-            if w is not None and w.shape[0] != head_dim:
+    def _check(self, head_dim: int, dev: int):
+        if self._device is not None and self._device != dev:
+            raise ValueError(f"the rotary is on cuda:{self._device}, the chunk on cuda:{dev}")
+        for name, n in self._dims.items():
+            if n != head_dim:
                 raise ValueError(f"{name} must have {head_dim} entries")
-        for name, x in (("table", self.table), ("q_weight", self.q_weight), ("k_weight", self.k_weight)):
-            if x is not None and x.device != device:
-                raise ValueError(f"{name} is on {x.device}, the chunk on {device}")
+
+
+# The checks below run at every call, beside kernels of a few microseconds: one
+# comparison of what is expected each, and the reason worked out only when it fails.
 
 
 def _data(t):
     return None if t is None else t.data_ptr()
 
 
-def _tensor(t, what, dtype, dims):
+def _device_of(t, what):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _refuse(t, what, dtype, shape, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"{what} must have {dims} dimensions, got {tuple(t.shape)}")
-
-
-def _rows(t, what, shape, device):
-    """Rows bf16 [batch, tokens, heads, D], last dimension contiguous, others strided."""
-    _tensor(t, what, torch.bfloat16, 4)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected {device}")
-    if t.stride(3) != 1:
-        raise ValueError(f"{what} must be contiguous in its last dimension")
-    strides = [0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()[:3])]
-    if t.numel() and (any(s % 8 for s in strides) or t.data_ptr() % 16):
-        raise ValueError(f"{what} must be 16-byte aligned, with strides that are multiples of 8 elements")
-    return loopkv_rows(t.data_ptr(), *strides)
+    raise ValueError(f"{what} is on {t.device}, expected cuda:{dev}")
 
 
-def _ints(t, what, shape, device, optional=False):
-    if t is None and optional:
-        return None
-    _tensor(t, what, torch.int32, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _is(t, dtype, shape, dev):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+
+
+def _rows(t, what, shape, dev):
+    """Rows bf16 [batch, tokens, heads, D], last dimension contiguous, others
+    strided: the C struct, and the first and one past the last byte they reach."""
+    if not _is(t, torch.bfloat16, shape, dev):
+        _refuse(t, what, torch.bfloat16, shape, dev)
+    b, n, h, d = shape
+    sb, st, sh, sd = t.stride()
+    if b == 1:
+        sb = 0
+    if n == 1:
+        st = 0
+    if h == 1:
+        sh = 0
+    ptr = t.data_ptr()
+    if ((sb | st | sh) & 7 or ptr & 15 or sd != 1) and t.numel():
+        raise ValueError(f"{what} must be contiguous in its last dimension, 16-byte aligned, with strides that are "
+                         "multiples of 8 elements")
+    return loopkv_rows(ptr, sb, st, sh), ptr, ptr + 2 * ((b - 1) * sb + (n - 1) * st + (h - 1) * sh + d)
+
+
+def _ints(t, what, shape, dev):
+    if not _is(t, torch.int32, shape, dev):
+        _refuse(t, what, torch.int32, shape, dev)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected {device}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _span(t):
-    """First and one past the last byte that a tensor reaches."""
-    if t.numel() == 0:
-        return t.data_ptr(), t.data_ptr()
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-
-
-def _overlap(a, b):
-    (a0, a1), (b0, b1) = _span(a), _span(b)
-    return a0 < b1 and b0 < a1
-
-
-def _output(out, what, shape, device, inputs, itself=None):
-    """The contiguous output, zeros if not given; apart from every input but `itself` (in place)."""
+def _output(out, what, shape, dev, inputs=(), itself=None):
+    """The contiguous output, zeros if not given.  It must lie apart from every
+    input (name, tensor, its rows) but ``itself``, which it may be (in place)."""
     if out is None:
-        return torch.zeros(shape, dtype=torch.bfloat16, device=device)
-    _tensor(out, what, torch.bfloat16, len(shape))
-    if tuple(out.shape) != tuple(shape) or not out.is_contiguous() or out.device != device:
-        raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor on {device}")
-    if out.data_ptr() % 16:
-        raise ValueError(f"{what} must be 16-byte aligned")
-    for name, x in inputs.items():
-        if x is None or not _overlap(out, x):
-            continue
-        if name == itself and x.data_ptr() == out.data_ptr() and x.is_contiguous():
-            continue
-        raise ValueError(f"{what} overlaps {name}")
+        return torch.zeros(shape, dtype=torch.bfloat16, device=f"cuda:{dev}")
+    if not _is(out, torch.bfloat16, shape, dev):
+        _refuse(out, what, torch.bfloat16, shape, dev)
+    ptr = out.data_ptr()
+    if not out.is_contiguous() or ptr & 15:
+        raise ValueError(f"{what} must be contiguous and 16-byte aligned")
+    end = ptr + 2 * out.numel()
+    for name, x, rows in inputs:
+        if x is not None and rows[1] < end and ptr < rows[2]:
+            if not (name == itself and rows[1] == ptr and x.is_contiguous()):
+                raise ValueError(f"{what} overlaps {name}")
     return out
 
 
-def _err(err_flag, device):
+def _apart(a, b):
+    """Whether two contiguous outputs share no byte."""
+    return a.data_ptr() + 2 * a.numel() <= b.data_ptr() or b.data_ptr() + 2 * b.numel() <= a.data_ptr()
+
+
+def _err(err_flag, dev):
     if err_flag is None:
         return None
-    _tensor(err_flag, "err_flag", torch.int32, err_flag.dim() if isinstance(err_flag, torch.Tensor) else 1)
-    if err_flag.numel() < 1 or err_flag.device != device:
-        raise ValueError(f"err_flag must be an int32 word on {device}")
-    return ctypes.c_void_p(err_flag.data_ptr())
-
-
-def _stream(stream, device):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-    return ctypes.c_void_p(s.cuda_stream)
+    if not isinstance(err_flag, torch.Tensor) or err_flag.dtype != torch.int32 or err_flag.numel() < 1 \
+            or err_flag.get_device() != dev:
+        raise ValueError(f"err_flag must be an int32 word on cuda:{dev}")
+    return err_flag.data_ptr()
 
 
 def _cell_device(kv: KVCells, loop: int, layer: int):
@@ -183,18 +189,23 @@ def _cell_device(kv: KVCells, loop: int, layer: int):
     arena = kv.arenas[kv.source_cell(loop * kv.num_layers + layer)]
     if arena is None:
         raise ValueError(f"cell ({loop}, {layer}) has no storage")
-    return arena.device
+    return _device_of(arena, "the cell's storage")
 
 
-def _call(name, device, *args):
-    with torch.cuda.device(device):
-        st = getattr(_lib, name)(*args)
+def _call(fn, name, dev, stream, *args):
+    """Call on the tensors' device, whichever is current, on its current stream
+    unless another of its streams is given."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
     if st:
         raise LoopKVError(st, name)
-
-
-def _ref(x):
-    return None if x is None else ctypes.byref(x)
 
 
 def loopkv_norm_rope(rotary: Rotary, q, k, start_pos, new_lens=None, q_out=None, k_out=None, err_flag=None,
@@ -203,28 +214,32 @@ def loopkv_norm_rope(rotary: Rotary, q, k, start_pos, new_lens=None, q_out=None,
     [B, T, Hkv, D] (either may be None) at positions start_pos[b] + i in one
     pass; returns (q_out, k_out).  Rows from new_lens[b] on are left as they are
     (zeros in new outputs).  q_out may be q and k_out may be k, where contiguous."""
-    first = q if q is not None else k
+    first, what = (q, "q") if q is not None else (k, "k")
     if first is None:
         raise ValueError("q or k is required")
-    _tensor(first, "q" if q is not None else "k", torch.bfloat16, 4)
-    batch, tokens, _, dim = (int(x) for x in first.shape)
-    dev = first.device
+    dev = _device_of(first, what)
+    if first.dim() != 4:
+        raise ValueError(f"{what} must be [batch, tokens, heads, head_dim]")
+    batch, tokens, _, dim = first.shape
     rotary._check(dim, dev)
-    heads = [0 if x is None or not isinstance(x, torch.Tensor) or x.dim() != 4 else int(x.shape[2]) for x in (q, k)]
-    rows = [None if x is None else _rows(x, what, (batch, tokens, n, dim), dev)
-            for x, what, n in ((q, "q", heads[0]), (k, "k", heads[1]))]
-    ins = {"q": q, "k": k}
+    heads, kv_heads, qr, kr, ins = 0, 0, None, None, []
     if q is not None:
-        q_out = _output(q_out, "q_out", q.shape, dev, ins, "q")
+        heads = q.shape[2]
+        qr = _rows(q, "q", (batch, tokens, heads, dim), dev)
+        ins.append(("q", q, qr))
     if k is not None:
-        k_out = _output(k_out, "k_out", k.shape, dev, ins, "k")
-    if q is not None and k is not None and _overlap(q_out, k_out):
+        kv_heads = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        kr = _rows(k, "k", (batch, tokens, kv_heads, dim), dev)
+        ins.append(("k", k, kr))
+    q_out = _output(q_out, "q_out", q.shape, dev, ins, "q") if q is not None else None
+    k_out = _output(k_out, "k_out", k.shape, dev, ins, "k") if k is not None else None
+    if q is not None and k is not None and not _apart(q_out, k_out):
         raise ValueError("q_out overlaps k_out")
-    _call("loopkv_norm_rope", dev, ctypes.byref(rotary.struct), dim, heads[0], heads[1], _ref(rows[0]), _ref(rows[1]),
-          _ints(start_pos, "start_pos", (batch,), dev), _ints(new_lens, "new_lens", (batch,), dev, True), batch, tokens,
-          _data(q_out) if q is not None else None, _data(k_out) if k is not None else None, _err(err_flag, dev),
-          _stream(stream, dev))
-    return (q_out if q is not None else None), (k_out if k is not None else None)
+    lens = None if new_lens is None else _ints(new_lens, "new_lens", (batch,), dev)
+    _call(_lib.loopkv_norm_rope, "loopkv_norm_rope", dev, stream, rotary.struct, dim, heads, kv_heads,
+          qr and qr[0], kr and kr[0], _ints(start_pos, "start_pos", (batch,), dev), lens, batch, tokens, _data(q_out),
+          _data(k_out), _err(err_flag, dev))
+    return q_out, k_out
 
 
 def loopkv_rope_append(kv: KVCells, loop: int, layer: int, rotary, q, k_new, v_new, block_table, start_pos,
@@ -232,26 +247,30 @@ def loopkv_rope_append(kv: KVCells, loop: int, layer: int, rotary, q, k_new, v_n
     """Append a chunk's keys (normed and rotated; as they are if rotary is None)
     and values bf16 [B, T, Hkv, D] to a stored cell at positions start_pos[b] ..
     start_pos[b] + new_lens[b] - 1, and norm and rotate its queries bf16
-    [B, T, H, D] (or None) in the same launch; returns q_out."""
+    [B, T, H, D] (or None) in the same launch; returns q_out (new: zeros where
+    there is no row)."""
     dev = _cell_device(kv, loop, layer)
-    _tensor(k_new, "k_new", torch.bfloat16, 4)
-    batch, tokens = int(k_new.shape[0]), int(k_new.shape[1])
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        raise ValueError("k_new must be [batch, tokens, heads, head_dim]")
+    batch, tokens = k_new.shape[:2]
     shape = (batch, tokens, kv.num_kv_heads, kv.head_dim)
     if rotary is not None:
         rotary._check(kv.head_dim, dev)
     elif q is not None:
         raise ValueError("q needs a rotary")
-    kr, vr = _rows(k_new, "k_new", shape, dev), _rows(v_new, "v_new", shape, dev)
-    qr = None
+    kr, vr, qr = _rows(k_new, "k_new", shape, dev), _rows(v_new, "v_new", shape, dev), None
     if q is not None:
-        qr = _rows(q, "q", (batch, tokens, kv.num_heads, kv.head_dim), dev)
-        q_out = _output(q_out, "q_out", q.shape, dev, {"q": q, "k_new": k_new, "v_new": v_new}, "q")
-    _call("loopkv_rope_append", dev, ctypes.byref(kv.cfg), ctypes.byref(kv.cells), loop, layer,
-          None if rotary is None else ctypes.byref(rotary.struct), _ref(qr), ctypes.byref(kr), ctypes.byref(vr),
+        shape = (batch, tokens, kv.num_heads, kv.head_dim)
+        qr = _rows(q, "q", shape, dev)
+        q_out = _output(q_out, "q_out", shape, dev, (("q", q, qr), ("k_new", k_new, kr), ("v_new", v_new, vr)), "q")
+    else:
+        q_out = None
+    lens = None if new_lens is None else _ints(new_lens, "new_lens", (batch,), dev)
+    _call(_lib.loopkv_rope_append, "loopkv_rope_append", dev, stream, kv.cfg, kv.cells, loop, layer,
+          rotary and rotary.struct, qr and qr[0], kr[0], vr[0],
           _ints(block_table, "block_table", (batch, kv.max_blocks_per_seq), dev),
-          _ints(start_pos, "start_pos", (batch,), dev), _ints(new_lens, "new_lens", (batch,), dev, True), batch, tokens,
-          _data(q_out) if q is not None else None, _err(err_flag, dev), _stream(stream, dev))
-    return q_out if q is not None else None
+          _ints(start_pos, "start_pos", (batch,), dev), lens, batch, tokens, _data(q_out), _err(err_flag, dev))
+    return q_out
 
 
 def loopkv_read_tokens(kv: KVCells, loop: int, layer: int, block_table, seq_lens, start_pos, num_tokens: int,
@@ -261,17 +280,19 @@ def loopkv_read_tokens(kv: KVCells, loop: int, layer: int, block_table, seq_lens
     Rows of tokens that are not there are left as they are (zeros in new
     outputs)."""
     dev = _cell_device(kv, loop, layer)
-    _tensor(start_pos, "start_pos", torch.int32, 1)
-    batch, num_tokens = int(start_pos.shape[0]), int(num_tokens)
-    shape = (batch, max(num_tokens, 0), kv.num_kv_heads, kv.head_dim)
-    outs = [_output(o, what, shape, dev, {}) for o, what in ((k_out, "k_out"), (v_out, "v_out"))]
-    if _overlap(*outs):
+    num_tokens = int(num_tokens)
+    if not isinstance(start_pos, torch.Tensor) or start_pos.dim() != 1 or num_tokens < 0:
+        raise ValueError("start_pos must be [batch], num_tokens not negative")
+    batch = start_pos.shape[0]
+    shape = (batch, num_tokens, kv.num_kv_heads, kv.head_dim)
+    k_out, v_out = _output(k_out, "k_out", shape, dev), _output(v_out, "v_out", shape, dev)
+    if not _apart(k_out, v_out):
         raise ValueError("k_out overlaps v_out")
-    _call("loopkv_read_tokens", dev, ctypes.byref(kv.cfg), ctypes.byref(kv.cells), loop, layer,
+    _call(_lib.loopkv_read_tokens, "loopkv_read_tokens", dev, stream, kv.cfg, kv.cells, loop, layer,
           _ints(block_table, "block_table", (batch, kv.max_blocks_per_seq), dev),
           _ints(seq_lens, "seq_lens", (batch,), dev), _ints(start_pos, "start_pos", (batch,), dev), batch, num_tokens,
-          _data(outs[0]), _data(outs[1]), _err(err_flag, dev), _stream(stream, dev))
-    return outs[0], outs[1]
+          k_out.data_ptr(), v_out.data_ptr(), _err(err_flag, dev))
+    return k_out, v_out
 
 
 def loopkv_chunk_attention(kv: KVCells, loop: int, layer: int, q, block_table, start_pos, new_lens=None,
@@ -284,20 +305,25 @@ def loopkv_chunk_attention(kv: KVCells, loop: int, layer: int, q, block_table, s
     rows up to its own.  Rows from new_lens[b] on are left as they are (zeros in
     a new output)."""
     dev = _cell_device(kv, loop, layer)
-    _tensor(q, "q", torch.bfloat16, 4)
-    batch, tokens = int(q.shape[0]), int(q.shape[1])
-    qr = _rows(q, "q", (batch, tokens, kv.num_heads, kv.head_dim), dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [batch, tokens, heads, head_dim]")
+    batch, tokens = q.shape[:2]
+    shape = (batch, tokens, kv.num_heads, kv.head_dim)
+    qr, kr, vr = _rows(q, "q", shape, dev), None, None
+    ins = [("q", q, qr)]
     if (k_cur is None) != (v_cur is None):
         raise ValueError("k_cur and v_cur come together")
-    kr = vr = None
     if k_cur is not None:
-        shape = (batch, tokens, kv.num_kv_heads, kv.head_dim)
-        kr, vr = _rows(k_cur, "k_cur", shape, dev), _rows(v_cur, "v_cur", shape, dev)
+        rows = (batch, tokens, kv.num_kv_heads, kv.head_dim)
+        kr, vr = _rows(k_cur, "k_cur", rows, dev), _rows(v_cur, "v_cur", rows, dev)
+        ins += [("k_cur", k_cur, kr), ("v_cur", v_cur, vr)]
     if out is None and new_lens is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)  # every row is written
-    out = _output(out, "out", q.shape, dev, {"q": q, "k_cur": k_cur, "v_cur": v_cur})
-    _call("loopkv_chunk_attention", dev, ctypes.byref(kv.cfg), ctypes.byref(kv.cells), loop, layer, ctypes.byref(qr),
-          _ref(kr), _ref(vr), _ints(block_table, "block_table", (batch, kv.max_blocks_per_seq), dev),
-          _ints(start_pos, "start_pos", (batch,), dev), _ints(new_lens, "new_lens", (batch,), dev, True), batch, tokens,
-          int(max_seq_len), float(sm_scale), _data(out), _err(err_flag, dev), _stream(stream, dev))
+        out = torch.empty(shape, dtype=torch.bfloat16, device=f"cuda:{dev}")  # every row is written
+    else:
+        out = _output(out, "out", shape, dev, ins)
+    lens = None if new_lens is None else _ints(new_lens, "new_lens", (batch,), dev)
+    _call(_lib.loopkv_chunk_attention, "loopkv_chunk_attention", dev, stream, kv.cfg, kv.cells, loop, layer, qr[0],
+          kr and kr[0], vr and vr[0], _ints(block_table, "block_table", (batch, kv.max_blocks_per_seq), dev),
+          _ints(start_pos, "start_pos", (batch,), dev), lens, batch, tokens, int(max_seq_len), float(sm_scale),
+          out.data_ptr(), _err(err_flag, dev))
     return out

@@ -173,14 +173,6 @@ def test_binding_refuses_host_tensors(m, c):
         m.Rotary(m.rope_table(8, 64, device="cpu"))
 
 
-def test_overlap_of_strided_rows(c):
-    base = torch.zeros(2, 3, 4 * 64)
-    a, b = base[..., :128], base[..., 128:]
-    assert c._overlap(a, b)             # they interleave
-    assert not c._overlap(base[0], base[1])
-    assert not c._overlap(base[:0], base)
-
-
 @pytest.mark.parametrize("rot", [16, 48, 64])
 def test_rope_table_agrees_with_oracle(m, rot):
     got = m.rope_table(5000, rot, device="cpu").numpy()
