@@ -35,7 +35,7 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
   auto kern = chunk_tensor_kernel<KIND, D, MT>;
   // At most as many CTAs an SM as its tensor memory serves (2 x 256 columns, or
   // one of 512): the request keeps further ones out, whose allocation would wait.
-  constexpr size_t kSmem = MT * (kTileKeys + D) > 256 && L::kBytes < 120 * 1024 ? 120 * 1024 : L::kBytes;
+  constexpr size_t kSmem = MT * (2 * kStepKeys + D) > 256 && L::kBytes < 120 * 1024 ? 120 * 1024 : L::kBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
   const int dev = current_device();
   {
@@ -45,6 +45,10 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
     if (dev < 0 || !done[dev]) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
+      // the registers that the groups of warps pass on are those of the launch
+      cudaFuncAttributes attr;
+      if (ChunkRegs<MT>::kMoves && (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != ChunkRegs<MT>::kLaunch))
+        return cudaErrorInvalidConfiguration;
       if (dev >= 0) done[dev] = true;
     }
   }
@@ -58,7 +62,7 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
   if (units * splits > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits), 1, 1);
-  cfg.blockDim = dim3(chunk_threads<D, MT>(), 1, 1);
+  cfg.blockDim = dim3(chunk_threads<MT>(), 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include "chunk_common.cuh"
 #include "tcgen05.cuh"
@@ -9,7 +10,8 @@
 namespace loopkv {
 
 constexpr int kTileKeys = 128;                       // keys of one tile: eight blocks
-constexpr int kDequantWarps = kTileKeys / kBlock;    // one block each
+constexpr int kStepKeys = 64;                        // keys of one step of products and softmax
+constexpr int kBlockWarps = kTileKeys / kBlock;      // dequantising warps, a block each
 constexpr int kExpRing = 4;
 
 // A block's keys (values) are stored as x 2^-e with e such that the largest is
@@ -24,20 +26,34 @@ struct ChunkSmem {
   static constexpr int kQ = 0;
   static constexpr int kK = MT * kTile;
   static constexpr int kV = kK + 2 * kTile;
-  static constexpr int kMeta = kV + 2 * kTile;       // per dequantising warp: key scales and minima, fp16
-  static constexpr int kKExp = kMeta + kDequantWarps * D * 4;
-  static constexpr int kVExp = kKExp + kExpRing * kDequantWarps * 4;
-  static constexpr int kStats = kVExp + kExpRing * kDequantWarps * 4;   // (max, sum) of each row
+  static constexpr int kMeta = kV + 2 * kTile;       // per key warp: its group's scales and minima, fp16
+  static constexpr int kKExp = kMeta + kBlockWarps * D * 4;            // 16-byte aligned
+  static constexpr int kVExp = kKExp + kExpRing * kBlockWarps * 4;
+  static constexpr int kStats = kVExp + kExpRing * kBlockWarps * 4;     // (max, sum) of each row
   static constexpr int kBars = kStats + MT * 128 * 8;
-  static constexpr int kBarCount = 8 + 3 * 2;
+  static constexpr int kBarCount = 9 + 2 * 6;
   static constexpr int kTmem = kBars + kBarCount * 8;
-  static constexpr int kFlags = kTmem + 4;           // value exponent of O, fault bits
-  static constexpr int kBytes = kFlags + 12;
+  static constexpr int kFlags = kTmem + 4;
+  static constexpr int kBytes = kFlags + 4;
   static constexpr int kPartial = kK;                // fp32 partial O over the stages: MT 128 D 4 = MT kTile 2 <= 4 kTile
 };
 
-template <int D, int MT>
-__host__ __device__ constexpr int chunk_threads() { return (MT * 4 + kDequantWarps + 1) * 32; }
+// Warps: four for the softmax of each 128 rows, eight that dequantise (a block
+// each), and four of which one issues the products: with MT = 2 registers move
+// between the groups of four warps, and the idle three bring theirs.
+template <int MT>
+__host__ __device__ constexpr int chunk_threads() { return (MT * 4 + kBlockWarps + 4) * 32; }
+
+// Registers a thread after the split.  They come out of what the block was
+// launched with, 65536 / threads rounded down to a multiple of 8 a thread:
+// MT = 2: 5 groups of 96 >= 2 x 136 + 2 x 80 + 48.  MT = 1: 4 of 128 each, as launched.
+template <int MT>
+struct ChunkRegs {
+  static constexpr int kSoftmax = MT == 2 ? 136 : 128, kDequant = MT == 2 ? 80 : 128, kIssue = MT == 2 ? 48 : 128;
+  static constexpr int kLaunch = 65536 / chunk_threads<MT>() / 8 * 8;
+  static constexpr bool kMoves = kSoftmax != kLaunch;
+  static_assert(MT * kSoftmax + 2 * kDequant + kIssue <= (MT + 3) * kLaunch, "register split");
+};
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
@@ -96,9 +112,44 @@ __device__ __forceinline__ uint32_t bf16x2_to_half(uint32_t w, float f) {
   return half2_bits(__floats2half2_rn(bf16_lo(w) * f, bf16_hi(w) * f));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two fp32 numbers side by side.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Bounded wait of a whole warp; the same answer for all its threads.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  bool done = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, done)) {
+    const unsigned long long t0 = global_timer_ns();
+#pragma unroll 1
+    do {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !done; ++i) done = mbar_try_wait(bar, parity);
+    } while (!done && global_timer_ns() - t0 <= kWaitTimeoutNs);
+  }
+  return __all_sync(0xffffffffu, done);
 }
 
 // What the CTA works on.
@@ -120,22 +171,39 @@ struct BlockLoader {
   static constexpr bool kQuant = KIND != LOOPKV_CELL_BF16;
   static constexpr bool kSplit = KIND == LOOPKV_CELL_Q4;
 
-  struct Raw {  // of one block, as loaded
-    uint32_t khi[KPL], klo[KPL], vhi[4], vlo[KPL], vmeta[KPL];
-    uint32_t kmeta[D / 32];
+  struct RawKeys {  // of one block, as loaded
+    uint32_t hi[KPL], lo[KPL], meta[D / 32];
+  };
+  struct RawValues {
+    uint32_t hi[4], lo[KPL], meta[KPL];
   };
 
   const ChunkAttnParams& p;
   const ChunkJob& job;
   int block, lane, c16, sub;
+  int key0;              // first of the thread's tokens as a key: key0 + SUBS i
+  int flip;              // its tokens as a value: sub KPL + (k ^ flip)
+  uint32_t key_at, value_at[2];   // their rows' places in the tile, first 16 bytes; the second are at ^ 16
 
+  // Where eight neighbouring threads would write rows of the same parity to
+  // the same banks, half of them take the other row of a pair.
   __device__ BlockLoader(const ChunkAttnParams& p, const ChunkJob& job, int block, int lane)
-      : p(p), job(job), block(block), lane(lane), c16(lane % C16), sub(lane / C16) {}
+      : p(p), job(job), block(block), lane(lane), c16(lane % C16), sub(lane / C16) {
+    key0 = D == 128 ? sub ^ (c16 >> 2) : sub;
+    flip = D == 128 ? c16 >> 2 : sub & 1;
+    key_at = swz(block * kBlock + key0, 2 * c16);
+    value_at[0] = swz(block * kBlock + sub * KPL + flip, 2 * c16);
+    value_at[1] = swz(block * kBlock + sub * KPL + (1 ^ flip), 2 * c16);
+  }
 
-  // The thread's tokens.  Where eight neighbouring threads would write rows of
-  // the same parity to the same banks, half of them take the other row first.
-  __device__ int key_token(int it) const { return it * SUBS + (D == 128 ? sub ^ (c16 >> 2) : sub); }
-  __device__ int value_token(int k) const { return sub * KPL + (k ^ (D == 128 ? c16 >> 2 : sub & 1)); }
+  __device__ int key_token(int it) const { return it * SUBS + key0; }
+  __device__ int value_token(int k) const { return sub * KPL + (k ^ flip); }
+  // a row SUBS (two) further on: as many rows of 128 bytes, and bit 2 (1) of the
+  // row turns in the swizzle
+  __device__ uint32_t key_place(int it) const {
+    return SUBS == 8 ? key_at + it * 1024 : ((key_at + it * 512) ^ ((it & 1) << 6));
+  }
+  __device__ uint32_t value_place(int k) const { return k < 2 ? value_at[k] : ((value_at[k & 1] + 256) ^ 32); }
 
   __device__ int token0(int tile) const { return tile * kTileKeys + block * kBlock; }
   // the key group of the block is full, so its keys are quantised
@@ -154,46 +222,53 @@ struct BlockLoader {
     return p.arena + (static_cast<size_t>(phys) * p.Hkv + job.hk) * R::kBytes;
   }
 
-  __device__ void load(int tile, int2 id, Raw& r) const {
+  __device__ void load(int tile, int2 id, RawKeys& r) const {
     const int t0 = token0(tile);
-    if (!kQuant || tile >= job.stored_tiles || t0 >= job.stored) return;
+    if (!kQuant || tile >= job.stored_tiles || !full(t0)) return;
     const uint8_t* rec = record(id.x);
-    if (full(t0)) {
-      const uint8_t* other = record(id.y);
-      // this thread's D / 32 channels of the group's scales
-      const int ch = lane * (D / 32);
-      const uint8_t* mrec = ((ch >= D / 2) == ((t0 & kBlock) != 0) ? rec : other) + R::kKMetaOff + (ch % (D / 2)) * 4;
-      if constexpr (D == 128) {
-        const uint4 w = *reinterpret_cast<const uint4*>(mrec);
-        r.kmeta[0] = w.x, r.kmeta[1] = w.y, r.kmeta[2] = w.z, r.kmeta[3] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(mrec);
-        r.kmeta[0] = w.x, r.kmeta[1] = w.y;
-      }
-#pragma unroll
-      for (int it = 0; it < KPL; ++it) {
-        const int at = key_token(it) * R::kRow + 4 * c16;
-        r.khi[it] = *reinterpret_cast<const uint32_t*>(rec + R::kKHi + at);
-        if constexpr (kSplit) r.klo[it] = *reinterpret_cast<const uint32_t*>(rec + R::kQ4KLo + at);
-      }
+    const uint8_t* other = record(id.y);
+    // this thread's D / 32 channels of the group's scales
+    const int ch = lane * (D / 32);
+    const uint8_t* mrec = ((ch >= D / 2) == ((t0 & kBlock) != 0) ? rec : other) + R::kKMetaOff + (ch % (D / 2)) * 4;
+    if constexpr (D == 128) {
+      const uint4 w = *reinterpret_cast<const uint4*>(mrec);
+      r.meta[0] = w.x, r.meta[1] = w.y, r.meta[2] = w.z, r.meta[3] = w.w;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(mrec);
+      r.meta[0] = w.x, r.meta[1] = w.y;
     }
+    const uint8_t* row = rec + key0 * R::kRow + 4 * c16;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint8_t* col = rec + R::kVHi + (4 * c16 + q) * kBlock + sub * KPL;
-      r.vhi[q] = KPL == 4 ? *reinterpret_cast<const uint32_t*>(col) : *reinterpret_cast<const uint16_t*>(col);
-    }
-#pragma unroll
-    for (int k = 0; k < KPL; ++k) {
-      const int t = value_token(k);
-      if constexpr (kSplit) r.vlo[k] = *reinterpret_cast<const uint32_t*>(rec + R::kQ4VLo + t * R::kRow + 4 * c16);
-      r.vmeta[k] = *reinterpret_cast<const uint32_t*>(rec + R::kVMetaOff + (t * (D / kGroup) + c16 / 2) * 4);
+    for (int it = 0; it < KPL; ++it) {
+      r.hi[it] = *reinterpret_cast<const uint32_t*>(row + R::kKHi + it * SUBS * R::kRow);
+      if constexpr (kSplit) r.lo[it] = *reinterpret_cast<const uint32_t*>(row + R::kQ4KLo + it * SUBS * R::kRow);
     }
   }
 
-  __device__ void store_row(uint32_t tile_base, int token, const uint32_t (&x)[8]) const {
-    const int r = block * kBlock + token;
-    st_shared16(tile_base + swz(r, 2 * c16), x[0], x[1], x[2], x[3]);
-    st_shared16(tile_base + swz(r, 2 * c16 + 1), x[4], x[5], x[6], x[7]);
+  __device__ void load(int tile, int2 id, RawValues& r) const {
+    const int t0 = token0(tile);
+    if (!kQuant || tile >= job.stored_tiles || t0 >= job.stored) return;
+    const uint8_t* rec = record(id.x);
+    const uint8_t* col = rec + R::kVHi + 4 * c16 * kBlock + sub * KPL;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      r.hi[q] = KPL == 4 ? *reinterpret_cast<const uint32_t*>(col + q * kBlock)
+                         : *reinterpret_cast<const uint16_t*>(col + q * kBlock);
+    constexpr int kMetaRow = (D / kGroup) * 4;
+    const uint8_t* lo[2] = {rec + R::kQ4VLo + value_token(0) * R::kRow + 4 * c16,
+                            rec + R::kQ4VLo + value_token(1) * R::kRow + 4 * c16};
+    const uint8_t* meta[2] = {rec + R::kVMetaOff + value_token(0) * kMetaRow + (c16 / 2) * 4,
+                              rec + R::kVMetaOff + value_token(1) * kMetaRow + (c16 / 2) * 4};
+#pragma unroll
+    for (int k = 0; k < KPL; ++k) {
+      if constexpr (kSplit) r.lo[k] = *reinterpret_cast<const uint32_t*>(lo[k & 1] + (k & 2) * R::kRow);
+      r.meta[k] = *reinterpret_cast<const uint32_t*>(meta[k & 1] + (k & 2) * kMetaRow);
+    }
+  }
+
+  __device__ static void store_row(uint32_t at, const uint32_t (&x)[8]) {
+    st_shared16(at, x[0], x[1], x[2], x[3]);
+    st_shared16(at ^ 16, x[4], x[5], x[6], x[7]);
   }
 
   // Exact bf16 rows into the tile; row(token) is the token's row or null (zeros).
@@ -228,13 +303,13 @@ struct BlockLoader {
         x[4 * j] = bf16x2_to_half(w[k][j].x, f), x[4 * j + 1] = bf16x2_to_half(w[k][j].y, f);
         x[4 * j + 2] = bf16x2_to_half(w[k][j].z, f), x[4 * j + 3] = bf16x2_to_half(w[k][j].w, f);
       }
-      store_row(tile_base, KEYS ? key_token(k) : value_token(k), x);
+      store_row(tile_base + (KEYS ? key_place(k) : value_place(k)), x);
     }
     return e;
   }
 
-  // Keys of the block; returns their exponent.
-  __device__ int store_keys(int tile, int2 id, const Raw& r, uint32_t tile_base, uint32_t meta) const {
+  // Keys of the block into the tile; returns their exponent.
+  __device__ int store(int tile, int2 id, const RawKeys& r, uint32_t tile_base, uint32_t meta) const {
     const int t0 = token0(tile);
     if (tile >= job.stored_tiles) {
       const int c0 = t0 - job.stored_tiles * kTileKeys;
@@ -255,7 +330,7 @@ struct BlockLoader {
       float s[CPT], mn[CPT], top = 0.f;
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
-        s[i] = bf16_lo(r.kmeta[i]), mn[i] = bf16_hi(r.kmeta[i]);
+        s[i] = bf16_lo(r.meta[i]), mn[i] = bf16_hi(r.meta[i]);
         top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(s[i], kTop, mn[i]))));
       }
       const int e = block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
@@ -287,9 +362,9 @@ struct BlockLoader {
 #pragma unroll
       for (int it = 0; it < KPL; ++it) {
         uint32_t x[8];
-        codes_to_half<kSplit>(r.khi[it], kSplit ? r.klo[it] : 0u, [&](int n) { return bits_half2(sw[n]); },
+        codes_to_half<kSplit>(r.hi[it], kSplit ? r.lo[it] : 0u, [&](int n) { return bits_half2(sw[n]); },
                               [&](int n) { return bits_half2(mw[n]); }, x);
-        store_row(tile_base, key_token(it), x);
+        store_row(tile_base + key_place(it), x);
       }
       return e;
     } else {
@@ -300,8 +375,8 @@ struct BlockLoader {
     }
   }
 
-  // Values of the block; returns their exponent.
-  __device__ int store_values(int tile, int2 id, const Raw& r, uint32_t tile_base) const {
+  // Values of the block into the tile; returns their exponent.
+  __device__ int store(int tile, int2 id, const RawValues& r, uint32_t tile_base) const {
     const int t0 = token0(tile);
     if (tile >= job.stored_tiles) {
       const int c0 = t0 - job.stored_tiles * kTileKeys;
@@ -315,7 +390,7 @@ struct BlockLoader {
 #pragma unroll
       for (int k = 0; k < KPL; ++k) {
         // what lies behind the last token is no value
-        const uint32_t w = t0 + value_token(k) < job.stored ? r.vmeta[k] : 0u;
+        const uint32_t w = t0 + value_token(k) < job.stored ? r.meta[k] : 0u;
         s[k] = bf16_lo(w), mn[k] = bf16_hi(w);
         top = fmaxf(top, fmaxf(fabsf(mn[k]), fabsf(fmaf(s[k], kTop, mn[k]))));
       }
@@ -323,14 +398,13 @@ struct BlockLoader {
       const float f = pow2f(-e), fs = f * (kSplit ? 0x1p24f : 0x1p22f);
 #pragma unroll
       for (int k = 0; k < KPL; ++k) {
-        const int b = D == 128 ? k ^ (c16 >> 2) : k ^ (sub & 1);  // byte of the token in the column words
-        const uint32_t sel = b | ((4 + b) << 4);
-        const uint32_t hi = __byte_perm(__byte_perm(r.vhi[0], r.vhi[1], sel), __byte_perm(r.vhi[2], r.vhi[3], sel), 0x5410);
+        const uint32_t sel = ((k & 1) ^ flip) * 0x11 + 0x40 + (k & 2) * 0x11;  // the token's byte of the column words
+        const uint32_t hi = __byte_perm(__byte_perm(r.hi[0], r.hi[1], sel), __byte_perm(r.hi[2], r.hi[3], sel), 0x5410);
         const __half2 sa = __float2half2_rn(s[k] * fs), sb = __float2half2_rn(s[k] * (fs * 0.0625f));
         const __half2 m = __float2half2_rn(mn[k] * f);
         uint32_t x[8];
-        codes_to_half<kSplit>(hi, kSplit ? r.vlo[k] : 0u, [&](int n) { return n & 1 ? sb : sa; }, [&](int) { return m; }, x);
-        store_row(tile_base, value_token(k), x);
+        codes_to_half<kSplit>(hi, kSplit ? r.lo[k] : 0u, [&](int n) { return n & 1 ? sb : sa; }, [&](int) { return m; }, x);
+        store_row(tile_base + value_place(k), x);
       }
       return e;
     } else {
@@ -345,15 +419,15 @@ struct BlockLoader {
 // ---------------------------------------------------------------- the kernel
 
 template <int KIND, int D, int MT>
-__global__ void __launch_bounds__(chunk_threads<D, MT>(), 1) chunk_tensor_kernel(const ChunkAttnParams p, int row_tiles,
+__global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(const __grid_constant__ ChunkAttnParams p, int row_tiles,
                                                                                int splits) {
   using L = ChunkSmem<D, MT>;
-  constexpr int kThreads = chunk_threads<D, MT>(), kRows = MT * 128;
-  constexpr int kTmemCols = MT * (kTileKeys + D) <= 256 ? 256 : 512;
-  constexpr int kSoftmaxWarps = MT * 4;
+  constexpr int kThreads = chunk_threads<MT>(), kRows = MT * 128;
+  constexpr int kTmemCols = MT * (2 * kStepKeys + D) <= 256 ? 256 : 512;
+  constexpr int kSoftmaxWarps = MT * 4, kIssueWarp = kSoftmaxWarps + kBlockWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = blockIdx.x % splits;
   const uint32_t unit = blockIdx.x / splits;
   const int tile = row_tiles - 1 - static_cast<int>(unit % row_tiles);  // the rows that see most come first
@@ -419,243 +493,295 @@ __global__ void __launch_bounds__(chunk_threads<D, MT>(), 1) chunk_tensor_kernel
   auto k_empty = [&](int s) { return bars + 16 + 8 * s; };
   auto v_full = [&](int s) { return bars + 32 + 8 * s; };
   auto v_empty = [&](int s) { return bars + 48 + 8 * s; };
-  auto s_full = [&](int m) { return bars + 64 + 8 * m; };
-  auto p_full = [&](int m) { return bars + 80 + 8 * m; };
-  auto o_done = [&](int m) { return bars + 96 + 8 * m; };
-  volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlags);  // [0]: O's value exponent, [1]: a wait gave up
+  const uint32_t q_full = bars + 64;
+  auto s_full = [&](int m) { return bars + 72 + 8 * m; };                       // logits of a step are there
+  auto s_free = [&](int m) { return bars + 88 + 8 * m; };                       // and have been read
+  auto p_full = [&](int m, int buf) { return bars + 104 + 16 * m + 8 * buf; };  // its weights are there
+  auto o_done = [&](int m, int buf) { return bars + 136 + 16 * m + 8 * buf; };  // and are in O
+  volatile int* gave_up = reinterpret_cast<volatile int*>(smem + L::kFlags);
   float* k_exp = reinterpret_cast<float*>(smem + L::kKExp);
   int* v_exp = reinterpret_cast<int*>(smem + L::kVExp);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(k_full(s), kDequantWarps);
+      mbar_init(k_full(s), kBlockWarps);
       mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), kDequantWarps);
+      mbar_init(v_full(s), kBlockWarps);
       mbar_init(v_empty(s), 1);
     }
+    mbar_init(q_full, kSoftmaxWarps);
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full(m), 1);
-      mbar_init(p_full(m), 4);
-      mbar_init(o_done(m), 1);
+      mbar_init(s_free(m), 4);
+      for (int buf = 0; buf < 2; ++buf) {
+        mbar_init(p_full(m, buf), 4);
+        mbar_init(o_done(m, buf), 1);
+      }
     }
     fence_mbar_init();
-    flags[1] = 0;
+    *gave_up = 0;
   }
-  if (warp == kSoftmaxWarps + kDequantWarps) tmem_alloc<kTmemCols>(sbase + L::kTmem);
-
-  // Queries: a row a thread, times a power of two that brings its largest entry
-  // to [2^13, 2^14) (bf16's 8 bits stay whole in fp16), sign of the scale with it.
-  float row_scale = 0.f;
-  if (warp < kSoftmaxWarps) {
-    const uint4* src = reinterpret_cast<const uint4*>(
-        row_at(p.q, job.b, my_row >> p.g_log2, (job.hk << p.g_log2) + (my_row & (G - 1))));
-    uint4 w[D / 8];
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) w[i] = src[i];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-      top = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(top, w[i].x), w[i].y), w[i].z), w[i].w);
-    const int e = max(static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127 - 13, -100);
-    const float f = p.sm_scale_log2 < 0.f ? -pow2f(-e) : pow2f(-e);
-    row_scale = fabsf(p.sm_scale_log2) * pow2f(e);
-    const uint32_t q = sbase + L::kQ + (warp / 4) * L::kTile;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-      st_shared16(q + swz(threadIdx.x % 128, i), bf16x2_to_half(w[i].x, f), bf16x2_to_half(w[i].y, f),
-                  bf16x2_to_half(w[i].z, f), bf16x2_to_half(w[i].w, f));
-    fence_proxy_async_shared();
-  }
-  __syncwarp();
+  if (warp == kIssueWarp) tmem_alloc<kTmemCols>(sbase + L::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // tensor memory: the logits of a step, two buffers of weights, the outputs
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmem);
-  const uint32_t tmem_o = tmem + MT * kTileKeys;
+  const uint32_t tmem_p = tmem + MT * kStepKeys, tmem_o = tmem + MT * 2 * kStepKeys;
   bool ok = true;
-  const int n = job.tiles;
+  const int n = job.tiles, steps = 2 * n;
+  // How the warps without rows end: what the join needs is then no burden on
+  // their registers.
+  auto leave = [&]() {
+    if (!ok && lane == 0) flag_error(p.chunk.err, LOOPKV_DEVERR_TIMEOUT);
+    __syncthreads();
+    if (warp == kIssueWarp) tmem_free<kTmemCols>(tmem);
+    if (splits > 1) {
+      cluster_sync_all();
+      cluster_sync_all();
+    }
+  };
 
-  if (warp >= kSoftmaxWarps && warp < kSoftmaxWarps + kDequantWarps) {
+  if (warp >= kSoftmaxWarps && warp < kIssueWarp) {
     // ------------------------------------------------------------ dequantise
+    set_max_registers<ChunkRegs<MT>::kDequant, ChunkRegs<MT>::kLaunch>();
     const int block = warp - kSoftmaxWarps;
     const BlockLoader<KIND, D> loader(p, job, block, lane);
-    typename BlockLoader<KIND, D>::Raw cur, next;
-    // the ids two tiles ahead, the records one
+    typename BlockLoader<KIND, D>::RawKeys keys = {};
+    typename BlockLoader<KIND, D>::RawValues values = {};
+    // The records' bytes come one tile ahead, each part into the registers that
+    // the tile before has just left; the block ids two tiles ahead.
     int2 id = n > 0 ? loader.ids(job.tile0) : make_int2(0, 0), id_next = n > 1 ? loader.ids(job.tile0 + 1) : id;
-    if (n > 0) loader.load(job.tile0, id, cur);
-    for (int j = 0; j < n && ok; ++j) {
-      const int s = j & 1, ring = j % kExpRing;
-      if (j + 1 < n) loader.load(job.tile0 + j + 1, id_next, next);
-      const int2 id_after = j + 2 < n ? loader.ids(job.tile0 + j + 2) : id_next;
-      if (j >= 2) ok = warp_wait(k_empty(s), ((j >> 1) - 1) & 1);
-      if (!ok) break;
-      const int ke = loader.store_keys(job.tile0 + j, id, cur, sbase + L::kK + s * L::kTile, sbase + L::kMeta + block * D * 4);
-      if (lane == 0) k_exp[ring * kDequantWarps + block] = pow2f(max(min(ke, 127), -149));
+    if (n > 0) {
+      loader.load(job.tile0, id, keys);
+      loader.load(job.tile0, id, values);
+    }
+    for (int j = 0; j < n; ++j) {
+      const int s = j & 1, t = job.tile0 + j, ring = j % kExpRing * kBlockWarps + block;
+      const int2 id_after = j + 2 < n ? loader.ids(t + 2) : id_next;
+      if (j >= 2 && !(ok = warp_wait(k_empty(s), ((j >> 1) - 1) & 1))) break;
+      int e = loader.store(t, id, keys, sbase + L::kK + s * L::kTile, sbase + L::kMeta + block * D * 4);
+      if (lane == 0) k_exp[ring] = pow2f(max(min(e, 127), -149));
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full(s));
-      if (j >= 2) ok = warp_wait(v_empty(s), ((j >> 1) - 1) & 1);
-      if (!ok) break;
-      const int ve = loader.store_values(job.tile0 + j, id, cur, sbase + L::kV + s * L::kTile);
-      if (lane == 0) v_exp[ring * kDequantWarps + block] = ve;
+      if (j + 1 < n) loader.load(t + 1, id_next, keys);
+      if (j >= 2 && !(ok = warp_wait(v_empty(s), ((j >> 1) - 1) & 1))) break;
+      e = loader.store(t, id, values, sbase + L::kV + s * L::kTile);
+      if (lane == 0) v_exp[ring] = e;
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full(s));
-      cur = next;
+      if (j + 1 < n) loader.load(t + 1, id_next, values);
       id = id_next;
       id_next = id_after;
     }
-  } else if (warp == kSoftmaxWarps + kDequantWarps) {
+    leave();
+    return;
+  }
+  if (warp >= kIssueWarp) {
     // ------------------------------------------------------------ multiply
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t kQKDesc = f16_idesc(kTileKeys, false), kPVDesc = f16_idesc(D, true);
-      auto issue_qk = [&](int m, int s) {
-        const uint32_t q = sbase + L::kQ + m * L::kTile, k = sbase + L::kK + s * L::kTile;
+    set_max_registers<ChunkRegs<MT>::kIssue, ChunkRegs<MT>::kLaunch>();
+    if (warp == kIssueWarp && n > 0) {
+      const uint32_t issue = elect_one();
+      constexpr uint32_t kQKDesc = f16_idesc(kStepKeys, false), kPVDesc = f16_idesc(D, true);
+      constexpr uint32_t kHalf = kStepKeys * 128;  // bytes between a tile's two steps
+      const uint64_t q_desc = smem_desc(sbase + L::kQ, 16), k_desc = smem_desc(sbase + L::kK, 16);
+      const uint64_t v_desc = smem_desc(sbase + L::kV, kTileKeys * 128);
+      auto issue_qk = [&](int m, int h) {
+        const uint64_t a = q_desc + ((m * L::kTile) >> 4);
+        const uint64_t b = k_desc + ((((h >> 1) & 1) * L::kTile + (h & 1) * kHalf) >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t at = (i / 4) * (kTileKeys * 128) + (i % 4) * 32;
-          mma_ss(tmem + m * kTileKeys, smem_desc(q + at, 16), smem_desc(k + at, 16), kQKDesc, i > 0);
+          constexpr int kSub = kTileKeys * 128;  // 64 channels further on
+          const uint32_t at = ((i / 4) * kSub + (i % 4) * 32) >> 4;
+          mma_ss(issue, tmem + m * kStepKeys, a + at, b + at, kQKDesc, i > 0);
         }
-        mma_commit(s_full(m));
+        mma_commit(issue, s_full(m));
       };
-      ok = mbar_wait(k_full(0), 0);
+      ok = warp_wait(q_full, 0) && warp_wait(k_full(0), 0);
       tc_fence_after();
-      if (ok) {
+      if (ok)
         for (int m = 0; m < MT; ++m) issue_qk(m, 0);
-        mma_commit(k_empty(0));
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        const int s = j & 1;
-        ok = mbar_wait(v_full(s), (j >> 1) & 1);
-        for (int m = 0; m < MT && ok; ++m) {
-          ok = mbar_wait(p_full(m), j & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t v = sbase + L::kV + s * L::kTile;
-#pragma unroll
-          for (int i = 0; i < kTileKeys / 16; ++i)
-            mma_ts(tmem_o + m * D, tmem + m * kTileKeys + i * 8, smem_desc(v + i * 2048, kTileKeys * 128), kPVDesc,
-                   j > 0 || i > 0);
-          mma_commit(o_done(m));
-          if (m == MT - 1) mma_commit(v_empty(s));
-          if (j + 1 < n) {
-            // the next logits take the columns of these weights
-            const int s1 = (j + 1) & 1;
-            if (m == 0) ok = mbar_wait(k_full(s1), ((j + 1) >> 1) & 1);
-            ok = ok && mbar_wait(o_done(m), j & 1);
+      for (int h = 0; h < steps && ok; ++h) {
+        if (h + 1 < steps) {  // the next step's logits, as soon as this one's have been read
+          if (h & 1) ok = warp_wait(k_full(((h + 1) >> 1) & 1), ((h + 1) >> 2) & 1);
+          for (int m = 0; m < MT && ok; ++m) {
+            ok = warp_wait(s_free(m), h & 1);
             if (!ok) break;
             tc_fence_after();
-            issue_qk(m, s1);
-            if (m == MT - 1) mma_commit(k_empty(s1));
+            issue_qk(m, h + 1);
           }
+          if (!ok) break;
+          if (!(h & 1)) mma_commit(issue, k_empty((h >> 1) & 1));
         }
+        if (!(h & 1)) ok = warp_wait(v_full((h >> 1) & 1), (h >> 2) & 1);
+        const uint64_t v = v_desc + ((((h >> 1) & 1) * L::kTile + (h & 1) * kHalf) >> 4);
+        for (int m = 0; m < MT && ok; ++m) {
+          ok = warp_wait(p_full(m, h & 1), (h >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t w = tmem_p + (2 * m + (h & 1)) * (kStepKeys / 2);
+#pragma unroll
+          for (int i = 0; i < kStepKeys / 16; ++i)
+            mma_ts(issue, tmem_o + m * D, w + i * 8, v + i * (2048 >> 4), kPVDesc, h > 0 || i > 0);
+          mma_commit(issue, o_done(m, h & 1));
+        }
+        if ((h & 1) && ok) mma_commit(issue, v_empty((h >> 1) & 1));
       }
     }
-    __syncwarp();
-  } else {
+    leave();
+    return;
+  }
+  {
     // ------------------------------------------------------------ softmax
+    set_max_registers<ChunkRegs<MT>::kSoftmax, ChunkRegs<MT>::kLaunch>();
     const int m = warp / 4;
     const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // tensor-memory lanes 32 (warp % 4) on
-    const uint32_t ts = tmem + m * kTileKeys + lanes, to = tmem_o + m * D + lanes;
+    const uint32_t ts = tmem + m * kStepKeys + lanes, tp = tmem_p + m * kStepKeys + lanes, to = tmem_o + m * D + lanes;
     const bool idle = row0 + warp * 32 >= row_end;                 // no row of this warp is there
     const int token = my_row >> p.g_log2;
+    // Queries: a row a thread, times a power of two that brings its largest entry
+    // to [2^13, 2^14) (bf16's 8 bits stay whole in fp16), the scale's sign with it.
+    float row_scale;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(row_at(p.q, job.b, token, (job.hk << p.g_log2) + (my_row & (G - 1))));
+      uint32_t top = 0;
+      uint4 w[D / 16];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) w[i] = src[half * (D / 16) + i];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          top = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(top, w[i].x), w[i].y), w[i].z), w[i].w);
+      }
+      const int e = max(static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127 - 13, -100);
+      const float f = p.sm_scale_log2 < 0.f ? -pow2f(-e) : pow2f(-e);
+      row_scale = fabsf(p.sm_scale_log2) * pow2f(e);
+      const uint32_t q = sbase + L::kQ + m * L::kTile;
+#pragma unroll
+      for (int half = 1; half >= 0; --half) {  // the second half is still here
+        if (half == 0)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) w[i] = src[i];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          st_shared16(q + swz(threadIdx.x % 128, half * (D / 16) + i), bf16x2_to_half(w[i].x, f), bf16x2_to_half(w[i].y, f),
+                      bf16x2_to_half(w[i].z, f), bf16x2_to_half(w[i].w, f));
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
     float m_ref = -INFINITY, sum = 0.f;
     int v_ref = -1000;
-    for (int j = 0; j < n && ok; ++j) {
-      const int gt = job.tile0 + j, ring = j % kExpRing;
-      ok = warp_wait(s_full(m), j & 1) && warp_wait(v_full(j & 1), (j >> 1) & 1);
+    for (int h = 0; h < steps && ok; ++h) {
+      const int j = h >> 1, buf = h & 1, gt = job.tile0 + j;
+      // the tile's exponents come with its keys and values
+      ok = (buf || (warp_wait(k_full(j & 1), (j >> 1) & 1) && warp_wait(v_full(j & 1), (j >> 1) & 1))) &&
+           warp_wait(s_full(m), h & 1);
       if (!ok) break;
-      if (!idle) {
-        tc_fence_after();
-        // keys of this tile that the row sees
-        const int lim = gt >= job.stored_tiles ? token + 1 - (gt - job.stored_tiles) * kTileKeys
-                        : (job.current ? job.stored : job.start + token + 1) - gt * kTileKeys;
-        const bool masked = __any_sync(0xffffffffu, lim < kTileKeys);
-        const float* ke = k_exp + ring * kDequantWarps;
-        const int* ve = v_exp + ring * kDequantWarps;
-        float top = -INFINITY;
-        uint32_t r[32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(ts + 32 * c, r);
-          tmem_wait_ld();
-          float a = -INFINITY, b = -INFINITY;
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= lim) r[i] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) a = fmaxf(a, __uint_as_float(r[i])), b = fmaxf(b, __uint_as_float(r[16 + i]));
-          // -inf times a scale of zero is no number: keep what is masked out of the product
-          if (a > -INFINITY) top = fmaxf(top, a * (row_scale * ke[2 * c]));
-          if (b > -INFINITY) top = fmaxf(top, b * (row_scale * ke[2 * c + 1]));
+      if (idle) {
+        if (lane == 0) {
+          mbar_arrive(s_free(m));
+          mbar_arrive(p_full(m, buf));
         }
-        int e_top = ve[0];
-#pragma unroll
-        for (int i = 1; i < kDequantWarps; ++i) e_top = max(e_top, ve[i]);
-        // The reference maximum follows the running one only when that is 2^8
-        // above it, the value exponent when a block is 2^4 above: weights stay
-        // below 2^12, and O is rescaled rarely.
-        const float m_new = top > m_ref + 8.f ? top : m_ref;
-        const int v_new = e_top > v_ref + 4 ? e_top : v_ref;
-        if (__any_sync(0xffffffffu, m_new != m_ref) || v_new != v_ref) {
-          const float shrink = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
-          sum *= shrink;
-          if (j > 0) {
-            ok = warp_wait(o_done(m), (j - 1) & 1);
-            tc_fence_after();
-            const float f = shrink * pow2f(max(v_ref - v_new, -149));
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              tmem_ld32(to + c, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-              tmem_st32(to + c, r);
-            }
-            tmem_wait_st();
-          }
-          m_ref = m_new;
-          v_ref = v_new;
-        }
-        const float base = m_ref == -INFINITY ? 0.f : m_ref;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(ts + 32 * c, r);
-          tmem_wait_ld();
-          uint32_t w[16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f = row_scale * ke[2 * c + h];
-            const int de = max(ve[2 * c + h] - v_ref, -100);
-            const float off = static_cast<float>(de) - base;
-            float part = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float x = fmaf(__uint_as_float(r[16 * h + i]), f, off), y = fmaf(__uint_as_float(r[16 * h + i + 1]), f, off);
-              if (masked) {
-                if (32 * c + 16 * h + i >= lim) x = -INFINITY;
-                if (32 * c + 16 * h + i + 1 >= lim) y = -INFINITY;
-              }
-              x = fast_exp2(x), y = fast_exp2(y);
-              part += x + y;
-              w[8 * h + i / 2] = half2_bits(__floats2half2_rn(x, y));
-            }
-            sum = fmaf(part, pow2f(-de), sum);
-          }
-          tmem_st16(ts + 16 * c, w);
-        }
-        tmem_wait_st();
-        tc_fence_before();
+        continue;
       }
+      tc_fence_after();
+      uint32_t r[kStepKeys];
+      tmem_ld64(ts, r);
+      tmem_wait_ld();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(m));
+      if (lane == 0) mbar_arrive(s_free(m));
+      // keys of this step that the row sees
+      const int lim = (gt >= job.stored_tiles ? token + 1 - (gt - job.stored_tiles) * kTileKeys
+                       : (job.current ? job.stored : job.start + token + 1) - gt * kTileKeys) - buf * kStepKeys;
+      const bool masked = __any_sync(0xffffffffu, lim < kStepKeys);
+      const float4 ke = *reinterpret_cast<const float4*>(k_exp + (j % kExpRing) * kBlockWarps + buf * 4);
+      const int4 ve = *reinterpret_cast<const int4*>(v_exp + (j % kExpRing) * kBlockWarps + buf * 4);
+      // a scale of zero (sm_scale, or exponents out of range) must not make a number of -inf
+      const float f[4] = {fmaxf(row_scale * ke.x, FLT_MIN), fmaxf(row_scale * ke.y, FLT_MIN),
+                          fmaxf(row_scale * ke.z, FLT_MIN), fmaxf(row_scale * ke.w, FLT_MIN)};
+      const int vexp[4] = {ve.x, ve.y, ve.z, ve.w};
+      if (masked) {
+        asm volatile("");  // a branch: most steps are not masked
+#pragma unroll
+        for (int i = 0; i < kStepKeys; ++i)
+          if (i >= lim) r[i] = 0xFF800000u;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t* x = r + 16 * c;
+        float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+        float b = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+        a = max3(a, __uint_as_float(x[6]), __uint_as_float(x[7]));
+        b = max3(b, __uint_as_float(x[8]), __uint_as_float(x[9]));
+        a = max3(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
+        b = max3(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
+        a = fmaxf(max3(a, __uint_as_float(x[14]), __uint_as_float(x[15])), b);
+        top = fmaxf(top, a * f[c]);
+      }
+      const int e_top = max(max(ve.x, ve.y), max(ve.z, ve.w));
+      // The reference maximum follows the running one only when that is 2^8
+      // above it, the value exponent when a block is 2^4 above: weights stay
+      // below 2^12, and O is rescaled rarely.
+      const float m_new = top > m_ref + 8.f ? top : m_ref;
+      const int v_new = e_top > v_ref + 4 ? e_top : v_ref;
+      if (__any_sync(0xffffffffu, m_new != m_ref) || v_new != v_ref) {
+        const float shrink = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+        sum *= shrink;
+        if (h > 0) {
+          ok = warp_wait(o_done(m, buf ^ 1), ((h - 1) >> 1) & 1);
+          tc_fence_after();
+          const float f = shrink * pow2f(max(v_ref - v_new, -149));
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(to + c, o);
+          }
+        }
+        m_ref = m_new;
+        v_ref = v_new;
+      }
+      // the weights' buffer: the products of two steps ago have read it
+      if (h >= 2) ok = ok && warp_wait(o_done(m, buf), ((h >> 1) - 1) & 1);
+      const float base = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int de = max(vexp[c] - v_ref, -100);  // at most 4
+        const float off = static_cast<float>(de) - base;
+        const uint64_t f2 = pack2(f[c], f[c]), off2 = pack2(off, off);
+        uint64_t part = 0;  // two sums of zero
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x, y;
+          unpack2(fma2(pack2(__uint_as_float(r[16 * c + 2 * i]), __uint_as_float(r[16 * c + 2 * i + 1])), f2, off2), x, y);
+          x = fast_exp2(x), y = fast_exp2(y);
+          part = add2(part, pack2(x, y));
+          w[i] = half2_bits(__floats2half2_rn(x, y));
+        }
+        float pa, pb;
+        unpack2(part, pa, pb);
+        sum = fmaf(pa + pb, __int_as_float((127 - de) << 23), sum);
+        tmem_st8(tp + buf * (kStepKeys / 2) + 8 * c, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(m, buf));
     }
     // ------------------------------------------------------------ results
-    if (n > 0 && ok) ok = warp_wait(o_done(m), (n - 1) & 1);
+    if (n > 0 && ok) ok = warp_wait(o_done(m, 1), (n - 1) & 1);
     tc_fence_after();
-    if (!ok) flags[1] = 1;
     if (!idle) {
       const float f = pow2f(max(min(v_ref, 127), -149)) * (splits == 1 ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
       const bool valid = row0 + threadIdx.x < row_end;
@@ -693,51 +819,49 @@ __global__ void __launch_bounds__(chunk_threads<D, MT>(), 1) chunk_tensor_kernel
       }
     }
   }
-  if (!ok && lane == 0) {
-    flags[1] = 1;
-    flag_error(p.chunk.err, LOOPKV_DEVERR_TIMEOUT);
-  }
+  if (!ok && lane == 0) flag_error(p.chunk.err, LOOPKV_DEVERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftmaxWarps + kDequantWarps) tmem_free<kTmemCols>(tmem);
   if (splits == 1) return;
 
   // ---------------------------------------------------------------- join the splits
   // Every CTA holds its partial rows (times their value exponent) and their
   // (max, sum); row i is put together by CTA i % splits from all of them.
   cluster_sync_all();
-  const uint32_t stats = sbase + L::kStats, partial = sbase + L::kPartial;
-  constexpr int kWarps = kThreads / 32, kQuads = D / 4, kRowsPerWarp = 32 / kQuads;
-  const int quad = lane % kQuads;
-  for (int i = warp * kRowsPerWarp + lane / kQuads; ; i += kWarps * kRowsPerWarp) {
-    const int row = i * splits + rank;
-    if (row0 + row >= row_end) break;
-    float m_all = -INFINITY;
-    for (int s = 0; s < splits; ++s) {
-      float pm;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pm) : "r"(peer_addr(stats + row * 8, s)));
-      m_all = fmaxf(m_all, pm);
+  {
+    const uint32_t stats = sbase + L::kStats, partial = sbase + L::kPartial;
+    constexpr int kQuads = D / 4, kRowsPerWarp = 32 / kQuads;
+    const int quad = lane % kQuads;
+    for (int i = warp * kRowsPerWarp + lane / kQuads;; i += kSoftmaxWarps * kRowsPerWarp) {
+      const int row = i * splits + rank;
+      if (row0 + row >= row_end) break;
+      float m_all = -INFINITY;
+      for (int s = 0; s < splits; ++s) {
+        float pm;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pm) : "r"(peer_addr(stats + row * 8, s)));
+        m_all = fmaxf(m_all, pm);
+      }
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < splits; ++s) {
+        float pm, ps;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(pm), "=f"(ps) : "r"(peer_addr(stats + row * 8, s)));
+        if (pm == -INFINITY) continue;  // it saw no key
+        const float wgt = fast_exp2(pm - m_all);
+        float4 x;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                     : "r"(peer_addr(partial + row * D * 4 + ((quad ^ (row & (kQuads - 1))) << 4), s)));
+        sum = fmaf(wgt, ps, sum);
+        acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
+        acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int r = row0 + row;
+      __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + (r >> p.g_log2)) * p.H +
+                                  (job.hk << p.g_log2) + (r & (G - 1))) * D;
+      reinterpret_cast<uint2*>(o)[quad] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < splits; ++s) {
-      float pm, ps;
-      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(pm), "=f"(ps) : "r"(peer_addr(stats + row * 8, s)));
-      if (pm == -INFINITY) continue;  // it saw no key
-      const float wgt = fast_exp2(pm - m_all);
-      float4 x;
-      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                   : "r"(peer_addr(partial + row * D * 4 + ((quad ^ (row & (kQuads - 1))) << 4), s)));
-      sum = fmaf(wgt, ps, sum);
-      acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
-      acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int r = row0 + row;
-    __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + (r >> p.g_log2)) * p.H +
-                                (job.hk << p.g_log2) + (r & (G - 1))) * D;
-    reinterpret_cast<uint2*>(o)[quad] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
   cluster_sync_all();
 }
