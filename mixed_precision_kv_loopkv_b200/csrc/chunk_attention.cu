@@ -1,7 +1,9 @@
 // Attention of a chunk of new tokens over a paged LoopKV cell (sm_100a): the
-// launch of the tensor-core kernel in chunk_tensor.cuh.
+// choice between the kernels of chunk_tensor.cuh (128 rows and more of a KV
+// head) and chunk_few.cuh (at most 16), and their launches.
 #include <mutex>
 
+#include "chunk_few.cuh"
 #include "chunk_tensor.cuh"
 
 namespace loopkv {
@@ -29,41 +31,15 @@ int sm_count(int dev) {
   return count[dev];
 }
 
-template <int KIND, int D, int MT>
-cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
-  using L = ChunkSmem<D, MT>;
-  auto kern = chunk_tensor_kernel<KIND, D, MT>;
-  // At most as many CTAs an SM as its tensor memory serves (2 x 256 columns, or
-  // one of 512): the request keeps further ones out, whose allocation would wait.
-  constexpr size_t kSmem = MT * (2 * kStepKeys + D) > 256 && L::kBytes < 120 * 1024 ? 120 * 1024 : L::kBytes;
-  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
-  const int dev = current_device();
-  {
-    static std::mutex mu;
-    static bool done[kMaxDevices] = {};
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || !done[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-      if (e != cudaSuccess) return e;
-      // the registers that the groups of warps pass on are those of the launch
-      cudaFuncAttributes attr;
-      if (ChunkRegs<MT>::kMoves && (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != ChunkRegs<MT>::kLaunch))
-        return cudaErrorInvalidConfiguration;
-      if (dev >= 0) done[dev] = true;
-    }
-  }
-  const int64_t rows = static_cast<int64_t>(p.chunk.T) << p.g_log2;
-  const int64_t row_tiles = (rows + MT * 128 - 1) / (MT * 128);
-  const int64_t units = row_tiles * p.Hkv * p.chunk.B;
-  const int64_t keys = static_cast<int64_t>(p.max_stored) + (p.k_cur.p ? p.chunk.T : 0);
-  const int64_t key_tiles = (keys + kTileKeys - 1) / kTileKeys;
-  int splits = 1;
-  while (splits < kMaxSplits && units * splits * 2 <= sm_count(dev) && key_tiles >= splits * 4) splits *= 2;
+// One launch of `units` groups of `splits` CTAs, a cluster each.
+template <typename Kernel, typename... Args>
+cudaError_t launch_clusters(Kernel kern, int64_t units, int splits, int threads, size_t smem, cudaStream_t stream,
+                            const ChunkAttnParams& p, Args... args) {
   if (units * splits > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits), 1, 1);
-  cfg.blockDim = dim3(chunk_threads<MT>(), 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   if (splits > 1) {
@@ -74,13 +50,75 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, kern, p, static_cast<int>(row_tiles), splits);
+  return cudaLaunchKernelEx(&cfg, kern, p, args..., splits);
+}
+
+// Shared-memory limit of a kernel (MT = 0: the one for few rows), once a device;
+// regs: registers that it must have been built with (0: any).
+template <int KIND, int D, int MT, typename Kernel>
+cudaError_t prepare_once(Kernel kern, size_t smem, int regs, int dev) {
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes attr;
+  if (regs && (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != regs))
+    return cudaErrorInvalidConfiguration;
+  if (dev >= 0) done[dev] = true;
+  return cudaSuccess;
+}
+
+template <int KIND, int D, int MT>
+cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
+  using L = ChunkSmem<D, MT>;
+  // At most as many CTAs an SM as its tensor memory serves (2 x 256 columns, or
+  // one of 512): the request keeps further ones out, whose allocation would wait.
+  constexpr size_t kSmem = MT * (2 * kStepKeys + D) > 256 && L::kBytes < 120 * 1024 ? 120 * 1024 : L::kBytes;
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+  const int dev = current_device();
+  // the registers that the groups of warps pass on are those of the launch
+  static constexpr auto kern = chunk_tensor_kernel<KIND, D, MT>;
+  const cudaError_t e = prepare_once<KIND, D, MT>(kern, kSmem, ChunkRegs<MT>::kMoves ? ChunkRegs<MT>::kLaunch : 0, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(p.chunk.T) << p.g_log2;
+  const int64_t row_tiles = (rows + MT * 128 - 1) / (MT * 128);
+  const int64_t units = row_tiles * p.Hkv * p.chunk.B;
+  const int64_t keys = static_cast<int64_t>(p.max_stored) + (p.k_cur.p ? p.chunk.T : 0);
+  const int64_t key_tiles = (keys + kTileKeys - 1) / kTileKeys;
+  int splits = 1;
+  while (splits < kMaxSplits && units * splits * 2 <= sm_count(dev) && key_tiles >= splits * 4) splits *= 2;
+  return launch_clusters(kern, units, splits, chunk_threads<MT>(), kSmem, stream, p, static_cast<int>(row_tiles));
+}
+
+// Few rows: the split with the fewest group times on the busiest SM, a CTA's
+// start and join counted as four.
+template <int KIND, int D>
+cudaError_t launch_few(const ChunkAttnParams& p, cudaStream_t stream) {
+  using L = FewSmem<KIND, D>;
+  static_assert(L::kBytes <= 227 * 1024, "shared memory of one CTA");
+  const int dev = current_device();
+  static constexpr auto kern = chunk_few_kernel<KIND, D>;
+  const cudaError_t e = prepare_once<KIND, D, 0>(kern, L::kBytes, 0, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t units = static_cast<int64_t>(p.Hkv) * p.chunk.B, sms = sm_count(dev);
+  const int64_t groups = (static_cast<int64_t>(p.max_stored) + kGroup - 1) / kGroup + (p.k_cur.p ? 1 : 0);
+  int splits = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kMaxSplits; s *= 2) {
+    const int64_t cost = (units * s + sms - 1) / sms * ((groups + s * kFewWarps - 1) / (s * kFewWarps) + 4);
+    if (cost < best) best = cost, splits = s;
+  }
+  return launch_clusters(kern, units, splits, kFewWarps * 32, L::kBytes, stream, p);
 }
 
 template <int KIND, int D>
 cudaError_t launch_t(const ChunkAttnParams& p, cudaStream_t stream) {
-  return (static_cast<int64_t>(p.chunk.T) << p.g_log2) > 128 ? launch_mt<KIND, D, 2>(p, stream)
-                                                             : launch_mt<KIND, D, 1>(p, stream);
+  const int64_t rows = static_cast<int64_t>(p.chunk.T) << p.g_log2;
+  if constexpr (KIND != LOOPKV_CELL_BF16)
+    if (rows <= kFewRows) return launch_few<KIND, D>(p, stream);
+  return rows > 128 ? launch_mt<KIND, D, 2>(p, stream) : launch_mt<KIND, D, 1>(p, stream);
 }
 
 }  // namespace

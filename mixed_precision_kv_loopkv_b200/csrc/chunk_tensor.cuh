@@ -161,6 +161,85 @@ struct ChunkJob {
   bool current;
 };
 
+// Where the tile's row (token, query head) goes.
+template <int D>
+__device__ __forceinline__ __nv_bfloat16* chunk_out(const ChunkAttnParams& p, const ChunkJob& job, int row) {
+  const int head = (job.hk << p.g_log2) + (row & ((1 << p.g_log2) - 1));
+  return p.out + ((static_cast<size_t>(job.b) * p.chunk.T + (row >> p.g_log2)) * p.H + head) * D;
+}
+
+// The job of a CTA with rows row0 .. row0 + max_rows - 1 of sequence job.b and KV
+// head job.hk: fills in the rest of it.  False where there is nothing left to
+// do: no such rows, or rows that are zeros (written here if `writer`) because
+// the sequence is skipped or at fault (flagged here if `report`).  The answer is
+// the same for all CTAs of the sequence: every block id of it is looked at.
+template <int D>
+__device__ bool chunk_job(const ChunkAttnParams& p, ChunkJob& job, int row0, int max_rows, bool report, bool writer) {
+  job.current = p.k_cur.p != nullptr;
+  job.start = p.chunk.start_pos[job.b];
+  job.len = p.chunk.new_lens ? p.chunk.new_lens[job.b] : p.chunk.T;
+  if (job.len < 0 || job.len > p.chunk.T) {
+    if (report && threadIdx.x == 0 && job.start >= 0) flag_error(p.chunk.err, LOOPKV_DEVERR_SEQ_LEN);
+    return false;
+  }
+  const int rows = min((job.len << p.g_log2) - row0, max_rows);
+  if (rows <= 0) return false;
+  const int64_t stored = static_cast<int64_t>(job.start) + (job.current ? 0 : job.len);
+  int fault = 0;
+  if (job.start >= 0) {
+    if (stored > p.max_stored) {
+      fault = LOOPKV_DEVERR_SEQ_LEN;
+    } else {
+      const int blocks = (static_cast<int>(stored) + kBlock - 1) / kBlock;
+      int bad = 0;
+      for (int i = threadIdx.x; i < blocks; i += blockDim.x) {
+        const int phys = p.block_table[static_cast<size_t>(job.b) * p.max_blocks + i];
+        bad |= phys < 0 || phys >= p.num_blocks;
+      }
+      if (__syncthreads_or(bad)) fault = LOOPKV_DEVERR_BLOCK_ID;
+    }
+    if (!fault) {
+      job.stored = static_cast<int>(stored);
+      return true;
+    }
+    if (report && threadIdx.x == 0) flag_error(p.chunk.err, fault);
+  }
+  if (writer)
+    for (int i = threadIdx.x; i < rows * (D / 8); i += blockDim.x)
+      reinterpret_cast<uint4*>(chunk_out<D>(p, job, row0 + i / (D / 8)))[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+  return false;
+}
+
+// Four channels of a row out of its splits' partial results: (max, sum) at
+// `stats` and channels at `part` in the shared memory of each CTA of the cluster.
+template <int D>
+__device__ __forceinline__ void join_splits(const ChunkAttnParams& p, const ChunkJob& job, int row, int quad, int splits,
+                                            uint32_t stats, uint32_t part) {
+  float top = -INFINITY;
+  for (int s = 0; s < splits; ++s) {
+    float m;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m) : "r"(peer_addr(stats, s)) : "memory");
+    top = fmaxf(top, m);
+  }
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < splits; ++s) {
+    float m, l;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(peer_addr(stats, s)) : "memory");
+    if (m == -INFINITY) continue;  // it saw no key
+    const float w = fast_exp2(m - top);
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(peer_addr(part, s)) : "memory");
+    sum = fmaf(w, l, sum);
+    acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  reinterpret_cast<uint2*>(chunk_out<D>(p, job, row))[quad] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
 // ---------------------------------------------------------------- dequantising warps
 
 // One block of 16 tokens: 16 channels a thread, KPL tokens a thread.
@@ -422,7 +501,7 @@ template <int KIND, int D, int MT>
 __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(const __grid_constant__ ChunkAttnParams p, int row_tiles,
                                                                                int splits) {
   using L = ChunkSmem<D, MT>;
-  constexpr int kThreads = chunk_threads<MT>(), kRows = MT * 128;
+  constexpr int kRows = MT * 128;
   constexpr int kTmemCols = MT * (2 * kStepKeys + D) <= 256 ? 256 : 512;
   constexpr int kSoftmaxWarps = MT * 4, kIssueWarp = kSoftmaxWarps + kBlockWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -435,52 +514,10 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
   ChunkJob job;
   job.hk = (unit / row_tiles) % p.Hkv;
   job.b = unit / row_tiles / p.Hkv;
-  job.current = p.k_cur.p != nullptr;
-  job.start = p.chunk.start_pos[job.b];
-  job.len = p.chunk.new_lens ? p.chunk.new_lens[job.b] : p.chunk.T;
-  const bool first_cta = tile == 0 && job.hk == 0 && rank == 0;
-  if (job.len < 0 || job.len > p.chunk.T) {
-    if (first_cta && threadIdx.x == 0 && job.start >= 0) flag_error(p.chunk.err, LOOPKV_DEVERR_SEQ_LEN);
-    return;
-  }
-  const int rows = job.len << p.g_log2, row0 = tile * kRows;
-  if (row0 >= rows) return;
-  const int row_end = min(rows, row0 + kRows), last_token = (row_end - 1) >> p.g_log2;
-  const int64_t stored64 = static_cast<int64_t>(job.start) + (job.current ? 0 : job.len);
-  bool zero = job.start < 0;
-  int fault = 0;
-  if (!zero && stored64 > p.max_stored) {
-    fault = LOOPKV_DEVERR_SEQ_LEN;
-    zero = true;
-  }
-  job.stored = zero ? 0 : static_cast<int>(stored64);
-  if (!zero) {
-    // every block of the sequence, so that all its rows are answered alike
-    const int blocks = (job.stored + kBlock - 1) / kBlock;
-    int bad = 0;
-    for (int i = threadIdx.x; i < blocks; i += kThreads) {
-      const int phys = p.block_table[static_cast<size_t>(job.b) * p.max_blocks + i];
-      bad |= phys < 0 || phys >= p.num_blocks;
-    }
-    if (__syncthreads_or(bad)) {
-      fault = LOOPKV_DEVERR_BLOCK_ID;
-      zero = true;
-    }
-  }
-  const int G = 1 << p.g_log2;
-  // this thread's row (softmax warps): row m * 128 + lane of the tile
-  const int my_row = min(row0 + threadIdx.x, row_end - 1);
-  if (zero) {
-    if (fault && threadIdx.x == 0) flag_error(p.chunk.err, fault);
-    if (rank == 0)
-      for (int i = threadIdx.x; i < (row_end - row0) * (D / 8); i += kThreads) {
-        const int r = row0 + i / (D / 8);
-        __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + (r >> p.g_log2)) * p.H +
-                                    (job.hk << p.g_log2) + (r & (G - 1))) * D;
-        reinterpret_cast<uint4*>(o)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
-      }
-    return;
-  }
+  const int row0 = tile * kRows;
+  if (!chunk_job<D>(p, job, row0, kRows, tile == 0 && job.hk == 0 && rank == 0, rank == 0)) return;
+  const int row_end = min(job.len << p.g_log2, row0 + kRows), last_token = (row_end - 1) >> p.g_log2;
+  const int my_row = min(row0 + static_cast<int>(threadIdx.x), row_end - 1);  // of the softmax warps' threads
   // keys that the tile's last row sees, 128 at a time; this CTA's share of them
   const int seen = job.current ? job.stored : min(job.stored, job.start + last_token + 1);
   job.stored_tiles = (seen + kTileKeys - 1) / kTileKeys;
@@ -645,7 +682,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     // to [2^13, 2^14) (bf16's 8 bits stay whole in fp16), the scale's sign with it.
     float row_scale;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(row_at(p.q, job.b, token, (job.hk << p.g_log2) + (my_row & (G - 1))));
+      const uint4* src = reinterpret_cast<const uint4*>(row_at(p.q, job.b, token, (job.hk << p.g_log2) + (my_row & ((1 << p.g_log2) - 1))));
       uint32_t top = 0;
       uint4 w[D / 16];
 #pragma unroll
@@ -786,8 +823,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       const float f = pow2f(max(min(v_ref, 127), -149)) * (splits == 1 ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
       const bool valid = row0 + threadIdx.x < row_end;
       const int local = threadIdx.x;
-      __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + token) * p.H + (job.hk << p.g_log2) +
-                                  (my_row & (G - 1))) * D;
+      __nv_bfloat16* o = chunk_out<D>(p, job, my_row);
       if (splits > 1) reinterpret_cast<float2*>(smem + L::kStats)[local] = make_float2(m_ref, sum);
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
@@ -835,32 +871,8 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     for (int i = warp * kRowsPerWarp + lane / kQuads;; i += kSoftmaxWarps * kRowsPerWarp) {
       const int row = i * splits + rank;
       if (row0 + row >= row_end) break;
-      float m_all = -INFINITY;
-      for (int s = 0; s < splits; ++s) {
-        float pm;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pm) : "r"(peer_addr(stats + row * 8, s)));
-        m_all = fmaxf(m_all, pm);
-      }
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < splits; ++s) {
-        float pm, ps;
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(pm), "=f"(ps) : "r"(peer_addr(stats + row * 8, s)));
-        if (pm == -INFINITY) continue;  // it saw no key
-        const float wgt = fast_exp2(pm - m_all);
-        float4 x;
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                     : "r"(peer_addr(partial + row * D * 4 + ((quad ^ (row & (kQuads - 1))) << 4), s)));
-        sum = fmaf(wgt, ps, sum);
-        acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
-        acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
-      }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const int r = row0 + row;
-      __nv_bfloat16* o = p.out + ((static_cast<size_t>(job.b) * p.chunk.T + (r >> p.g_log2)) * p.H +
-                                  (job.hk << p.g_log2) + (r & (G - 1))) * D;
-      reinterpret_cast<uint2*>(o)[quad] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      join_splits<D>(p, job, row0 + row, quad, splits, stats + row * 8,
+                     partial + row * D * 4 + ((quad ^ (row & (kQuads - 1))) << 4));
     }
   }
   cluster_sync_all();
