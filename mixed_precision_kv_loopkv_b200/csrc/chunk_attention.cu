@@ -93,7 +93,7 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
 }
 
 // Few rows: the split with the fewest group times on the busiest SM, a CTA's
-// start and join counted as four.
+// start and join counted as two.
 template <int KIND, int D>
 cudaError_t launch_few(const ChunkAttnParams& p, cudaStream_t stream) {
   using L = FewSmem<KIND, D>;
@@ -107,7 +107,7 @@ cudaError_t launch_few(const ChunkAttnParams& p, cudaStream_t stream) {
   int splits = 1;
   int64_t best = INT64_MAX;
   for (int s = 1; s <= kMaxSplits; s *= 2) {
-    const int64_t cost = (units * s + sms - 1) / sms * ((groups + s * kFewWarps - 1) / (s * kFewWarps) + 4);
+    const int64_t cost = (units * s + sms - 1) / sms * ((groups + s * kFewWarps - 1) / (s * kFewWarps) + 2);
     if (cost < best) best = cost, splits = s;
   }
   return launch_clusters(kern, units, splits, kFewWarps * 32, L::kBytes, stream, p);

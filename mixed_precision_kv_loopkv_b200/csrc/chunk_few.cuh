@@ -59,7 +59,8 @@ struct FewWarp {
   static constexpr bool kSplit = KIND == LOOPKV_CELL_Q4;
   static constexpr int PAIRS = D / 8, STEPS = D / 16, CH = D / 8;
   static constexpr float kTop = kSplit ? 15.f : 3.f;
-  static constexpr float kUnit = kSplit ? 0x1p24f : 0x1p22f;   // codes stand 2 bits higher in 2-bit cells
+  static constexpr int kUnit = kSplit ? 24 : 22;               // codes stand 2 bits higher in 2-bit cells
+  static constexpr float kPerUnit = kSplit ? 0x1p-24f : 0x1p-22f;
 
   const ChunkAttnParams& p;
   const ChunkJob& job;
@@ -124,7 +125,7 @@ struct FewWarp {
       top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(sc[i], kTop, mn[i]))));
     }
     const int e = block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    const float f = pow2f(-e), fs = f * kUnit;
+    const float fs = block_unit<kUnit>(e), f = fs * kPerUnit;
     // pairs of channels: [scale, min] words, a pair's scale 2^24 or 2^20 times its
     // value by its place; four pairs of scales, then of minima, for each thread r
 #pragma unroll
@@ -141,9 +142,10 @@ struct FewWarp {
     // this thread's words of its four keys: D / 4 channels of two bits
     constexpr int WORDS = D / 64;
     uint32_t hi[4][WORDS], lo[4][WORDS];
+    const uint8_t* row0 = rec + few_key(quad, 0) * R::kRow + r * (D / 16);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const uint8_t* row = rec + (n >> 1) * R::kBytes + few_key(quad, n & 1) * R::kRow + r * (D / 16);
+      const uint8_t* row = row0 + (n >> 1) * R::kBytes + (n & 1) * R::kRow;
 #pragma unroll
       for (int w = 0; w < WORDS; ++w) {
         hi[n][w] = reinterpret_cast<const uint32_t*>(row + R::kKHi)[w];
@@ -207,7 +209,7 @@ struct FewWarp {
   // Logits to weights, in place: p 2^(ve - v_ref) as fp16 pairs a[block][4], the
   // products' left operand.  lim[i]: keys of the group that row quad + 8 i sees.
   __device__ void weights(float (&s)[4][4], int ke, int ve, const int (&lim)[2], uint32_t (&a)[2][4]) {
-    const float k = pow2f(max(min(ke, 127), -149));
+    const float k = block_scale(ke);
     bool masked = __any_sync(0xffffffffu, lim[0] < kGroup || lim[1] < kGroup);
     if (masked) {
       asm volatile("");
@@ -258,47 +260,54 @@ struct FewWarp {
     }
   }
 
-  // Largest exponent of the group's stored values; tokens from n on are none.
-  __device__ int quant_value_exp(const uint8_t* rec, int n) const {
+  // (scale, min) words of the thread's tokens (4 r .. of each block) and channels;
+  // tokens from n on are no values.  Returns the exponent of the group's values.
+  __device__ int quant_value_meta(const uint8_t* rec, int n, uint32_t (&meta)[2][4]) const {
+    const uint8_t* at = rec + R::kVMetaOff + (4 * r * (D / kGroup) + quad * CH / kGroup) * 4;
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / kGroup; ++i) {  // 32 tokens, D / 32 words each
-      const int at = lane + 32 * i, t = at / (D / kGroup);
-      uint32_t w = reinterpret_cast<const uint32_t*>(rec + (t / kBlock) * R::kBytes + R::kVMetaOff)[at % (kBlock * (D / kGroup))];
-      if (t >= n) w = 0u;
-      const float s = bf16_lo(w), mn = bf16_hi(w);
-      top = fmaxf(top, fmaxf(fabsf(mn), fabsf(fmaf(s, kTop, mn))));
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        meta[blk][t] = *reinterpret_cast<const uint32_t*>(at + blk * R::kBytes + t * (D / kGroup) * 4);
+    if (n < kGroup) {
+      asm volatile("");  // a branch: most groups are full
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((i >> 2) * kBlock + 4 * r + (i & 3) >= n) meta[i >> 2][i & 3] = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = bf16_lo(meta[i >> 2][i & 3]), mn = bf16_hi(meta[i >> 2][i & 3]);
+      top = max3(top, fabsf(mn), fabsf(fmaf(s, kTop, mn)));
     }
     return block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
   }
 
-  __device__ void quant_output(const uint8_t* rec, int n, int e, const uint32_t (&a)[2][4]) {
-    const float f = pow2f(-e), fs = f * kUnit;
+  __device__ void quant_output(const uint8_t* rec, const uint32_t (&meta)[2][4], int e, const uint32_t (&a)[2][4]) {
+    const float fs = block_unit<kUnit>(e), f = fs * kPerUnit, fs4 = fs * 0.0625f;
     constexpr int COLS = D / 32;  // words of four channels that a thread has of a token quad
+    const uint8_t* col = rec + R::kVHi + COLS * quad * kBlock + 4 * r;
+    const uint8_t* row = rec + R::kQ4VLo + 4 * r * R::kRow + quad * (CH / 4);
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-      const uint8_t* rb = rec + blk * R::kBytes;
       uint32_t hi[COLS], lo[4];
       float s[4], mn[4];
 #pragma unroll
-      for (int c = 0; c < COLS; ++c)
-        hi[c] = *reinterpret_cast<const uint32_t*>(rb + R::kVHi + (COLS * quad + c) * kBlock + 4 * r);
+      for (int c = 0; c < COLS; ++c) hi[c] = *reinterpret_cast<const uint32_t*>(col + blk * R::kBytes + c * kBlock);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int tok = 4 * r + t;
         if constexpr (kSplit) {
-          const uint8_t* at = rb + R::kQ4VLo + tok * R::kRow + quad * (CH / 4);
+          const uint8_t* at = row + blk * R::kBytes + t * R::kRow;
           lo[t] = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
         }
-        uint32_t w = *reinterpret_cast<const uint32_t*>(rb + R::kVMetaOff + (tok * (D / kGroup) + quad * CH / kGroup) * 4);
-        if (blk * kBlock + tok >= n) w = 0u;  // what lies behind the last token is no value
-        s[t] = bf16_lo(w), mn[t] = bf16_hi(w);
+        s[t] = bf16_lo(meta[blk][t]), mn[t] = bf16_hi(meta[blk][t]);
       }
       uint32_t b[CH][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // tokens (0, 2), (1, 3) of the four
         const __half2 sa = __floats2half2_rn(s[h] * fs, s[h + 2] * fs);
-        const __half2 sb = __floats2half2_rn(s[h] * (fs * 0.0625f), s[h + 2] * (fs * 0.0625f));
+        const __half2 sb = __floats2half2_rn(s[h] * fs4, s[h + 2] * fs4);
         const __half2 m = __floats2half2_rn(mn[h] * f, mn[h + 2] * f);
 #pragma unroll
         for (int c8 = 0; c8 < CH / 8; ++c8) {  // eight channels
@@ -306,8 +315,8 @@ struct FewWarp {
           uint32_t even, odd;
           if constexpr (kSplit) {
             const uint32_t wl = __byte_perm(lo[h], lo[h + 2], c8 ? 0x7632 : 0x5410);
-            even = ((wh << 2) & 0xCCCCCCCCu) | (wl & 0x33333333u);
-            odd = (wh & 0xCCCCCCCCu) | ((wl >> 2) & 0x33333333u);
+            even = join_bits(wh << 2, wl);
+            odd = join_bits(wh, wl >> 2);
           } else {
             even = (wh << 2) & 0xCCCCCCCCu;
             odd = wh & 0xCCCCCCCCu;
@@ -457,9 +466,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) chunk_few_kernel(const __gr
       const __nv_bfloat16* res = p.residual + (static_cast<size_t>(job.b) * p.Hkv + job.hk) * kGroup * D;
       ke = w.exact_logits([&](int t) { return t0 + t < job.stored ? res + t * D : nullptr; }, logit);
     }
-    const int ve = w.quant_value_exp(rec, job.stored - t0);
+    uint32_t value_meta[2][4];
+    const int ve = w.quant_value_meta(rec, job.stored - t0, value_meta);
     w.weights(logit, ke, ve, lim, a);
-    w.quant_output(rec, job.stored - t0, ve, a);
+    w.quant_output(rec, value_meta, ve, a);
   }
   if (!ok) {  // later copies must not land in memory that has another use
     for (int s = 0; s < kFewStages; ++s) warp_wait(bar + 8 * s, 0), warp_wait(bar + 8 * s, 1);

@@ -69,6 +69,23 @@ __device__ __forceinline__ int block_exp(uint32_t abs_bits) {
   return max(static_cast<int>(abs_bits >> 23) - 127 - kTopExp + 1, -100);
 }
 
+// The upper two bits of each nibble from hi, the lower two from lo: one
+// operation (mask ? hi : lo).
+__device__ __forceinline__ uint32_t join_bits(uint32_t hi, uint32_t lo) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(d) : "r"(0xCCCCCCCCu), "r"(hi), "r"(lo));
+  return d;
+}
+
+// 2^(k - e) for the exponent e of a block, k in [20, 24]: a normal number.
+template <int K>
+__device__ __forceinline__ float block_unit(int e) {
+  static_assert(K >= 20 && K <= 24, "e is in [-100, 134]");
+  return __int_as_float((127 + K - e) << 23);
+}
+// 2^e, at most 2^127 (keys beyond 2^120 have no finite logits anyway).
+__device__ __forceinline__ float block_scale(int e) { return __int_as_float((min(e, 127) + 127) << 23); }
+
 // 16 channels' codes (hi << 2 | lo, two bits each plane; 2-bit cells: code << 2)
 // as fp16 x = code s + m: eight half2 words of neighbouring channels.  s, m:
 // scale and minimum of each channel pair; the scale of a pair is 2^24 or 2^20
@@ -77,8 +94,8 @@ template <bool SPLIT, typename S, typename M>
 __device__ __forceinline__ void codes_to_half(uint32_t hi, uint32_t lo, S&& s, M&& m, uint32_t (&out)[8]) {
   uint32_t even, odd;  // nibble n: channel 2 n, 2 n + 1
   if constexpr (SPLIT) {
-    even = ((hi << 2) & 0xCCCCCCCCu) | (lo & 0x33333333u);
-    odd = (hi & 0xCCCCCCCCu) | ((lo >> 2) & 0x33333333u);
+    even = join_bits(hi << 2, lo);
+    odd = join_bits(hi, lo >> 2);
   } else {
     even = (hi << 2) & 0xCCCCCCCCu;
     odd = hi & 0xCCCCCCCCu;
@@ -413,7 +430,7 @@ struct BlockLoader {
         top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(s[i], kTop, mn[i]))));
       }
       const int e = block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      const float f = pow2f(-e), fs = f * (kSplit ? 0x1p24f : 0x1p22f);
+      const float fs = block_unit<kSplit ? 24 : 22>(e), f = fs * (kSplit ? 0x1p-24f : 0x1p-22f);
       // pair n of eight channels: 2^24 for even n, 2^20 for odd; parts of 16 bytes
       // [scale 0-7][scale 8-15][min 0-7][min 8-15] x C16 so that reads do not collide
 #pragma unroll
@@ -474,7 +491,7 @@ struct BlockLoader {
         top = fmaxf(top, fmaxf(fabsf(mn[k]), fabsf(fmaf(s[k], kTop, mn[k]))));
       }
       const int e = block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      const float f = pow2f(-e), fs = f * (kSplit ? 0x1p24f : 0x1p22f);
+      const float fs = block_unit<kSplit ? 24 : 22>(e), f = fs * (kSplit ? 0x1p-24f : 0x1p-22f);
 #pragma unroll
       for (int k = 0; k < KPL; ++k) {
         const uint32_t sel = ((k & 1) ^ flip) * 0x11 + 0x40 + (k & 2) * 0x11;  // the token's byte of the column words
@@ -598,7 +615,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       const int2 id_after = j + 2 < n ? loader.ids(t + 2) : id_next;
       if (j >= 2 && !(ok = warp_wait(k_empty(s), ((j >> 1) - 1) & 1))) break;
       int e = loader.store(t, id, keys, sbase + L::kK + s * L::kTile, sbase + L::kMeta + block * D * 4);
-      if (lane == 0) k_exp[ring] = pow2f(max(min(e, 127), -149));
+      if (lane == 0) k_exp[ring] = block_scale(e);
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full(s));
