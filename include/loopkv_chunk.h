@@ -66,7 +66,7 @@ typedef struct {
   int32_t interleaved;      /* 0: pairs half of rotary_dim apart, 1: neighbours */
   const void* q_weight;     /* device bf16 [head_dim], or NULL: queries not normed */
   const void* k_weight;     /* the same for keys */
-  double eps;               /* >= 0 */
+  double eps;               /* at least 1e-30 where there is a weight (a row of zeros has a norm then) */
 } loopkv_rotary;
 
 /*
@@ -76,7 +76,7 @@ typedef struct {
  *   start_pos    : device int32 [batch];  new_lens: optional device int32 [batch]
  *   q_out, k_out : device bf16 [batch][num_tokens][heads][D]
  * Errors: INVALID_ARG for null or misaligned pointers, bad strides, a bad
- * rotary (rotary_dim, max_positions <= 0, eps < 0 or NaN), negative sizes;
+ * rotary (rotary_dim, max_positions <= 0, eps below 1e-30 or not finite), negative sizes;
  * UNSUPPORTED for head_dim other than 64 and 128 or 2^31 rows or more.
  */
 LOOPKV_API loopkv_status loopkv_norm_rope(const loopkv_rotary* rotary, int32_t head_dim, int32_t num_heads,

@@ -16,11 +16,11 @@ struct RowView {
 };
 
 struct RotaryView {
-  const float* cos_sin;          // [max_positions][rot], null: no rotation
+  const float* cos_sin;          // [max_positions][rot]
   const __nv_bfloat16* q_weight;
   const __nv_bfloat16* k_weight;
   double eps;
-  int max_positions, rot, interleaved;
+  int max_positions, rot, interleaved;  // rot 0: no rotation
 };
 
 // Which tokens of the chunk a sequence has, and how far its positions may go.

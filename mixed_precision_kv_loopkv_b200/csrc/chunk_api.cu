@@ -29,14 +29,14 @@ loopkv_status check_rotary(const loopkv_rotary* r, int head_dim) {
     return LOOPKV_ERR_INVALID_ARG;
   if (r->interleaved != 0 && r->interleaved != 1) return LOOPKV_ERR_INVALID_ARG;
   if ((r->q_weight && !aligned16(r->q_weight)) || (r->k_weight && !aligned16(r->k_weight))) return LOOPKV_ERR_INVALID_ARG;
-  if (!(r->eps >= 0.0) || !isfinite(r->eps)) return LOOPKV_ERR_INVALID_ARG;
+  if ((r->q_weight || r->k_weight) && (!(r->eps >= 1e-30) || !isfinite(r->eps))) return LOOPKV_ERR_INVALID_ARG;
   return LOOPKV_OK;
 }
 
 RotaryView view(const loopkv_rotary* r) {
   if (!r) return RotaryView{nullptr, nullptr, nullptr, 0.0, 0, 0, 0};
   return RotaryView{r->cos_sin, static_cast<const __nv_bfloat16*>(r->q_weight),
-                    static_cast<const __nv_bfloat16*>(r->k_weight), r->eps, r->max_positions, r->rotary_dim,
+                    static_cast<const __nv_bfloat16*>(r->k_weight), r->eps, r->max_positions, r->cos_sin ? r->rotary_dim : 0,
                     r->interleaved};
 }
 

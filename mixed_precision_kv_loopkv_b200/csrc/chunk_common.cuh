@@ -41,8 +41,12 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   }
 }
 
+// Two floats as bf16, to nearest even, in one conversion (that of a single one
+// runs at an eighth of its rate).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return static_cast<uint32_t>(bf16_bits_rn(lo)) | (static_cast<uint32_t>(bf16_bits_rn(hi)) << 16);
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {

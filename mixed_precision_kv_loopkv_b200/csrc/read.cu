@@ -10,9 +10,22 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// (scale, min) word of a group and a 2- or 4-bit code -> value
-__device__ __forceinline__ float stands_for(uint32_t meta, uint32_t code) {
-  return fmaf(bf16_lo(meta), static_cast<float>(code), bf16_hi(meta));
+// Eight channels' codes (two bits of each in hi and, of 4-bit cells, in lo) and
+// their (scale, min) words -> values.  A code becomes a float as the low bits of
+// 2^23 (the conversion instruction runs at a quarter of the rate).
+template <bool SPLIT, typename Meta>
+__device__ __forceinline__ uint4 stand_for(uint32_t hi, uint32_t lo, Meta&& meta) {
+  constexpr uint32_t kMask = SPLIT ? 15u : 3u;
+  // nibble n: channel 2 n, 2 n + 1
+  const uint32_t even = SPLIT ? ((hi << 2) & 0xCCCCu) | (lo & 0x3333u) : hi;
+  const uint32_t odd = SPLIT ? (hi & 0xCCCCu) | ((lo >> 2) & 0x3333u) : hi >> 2;
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = meta(i), code = ((i & 1 ? odd : even) >> (4 * (i / 2))) & kMask;
+    x[i] = fmaf(bf16_lo(m), __uint_as_float(code | 0x4B000000u) - 8388608.f, bf16_hi(m));
+  }
+  return pack8(x);
 }
 
 template <int KIND, int D>
@@ -93,26 +106,14 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
                                                            ((8 * sub) % (D / 2)) * 4);
           const uint4 m0 = mp[0], m1 = mp[1];
           const uint32_t m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t hh = (hi >> (2 * i)) & 3u;
-            x[i] = stands_for(m[i], kSplit ? (hh << 2) | ((lo >> (2 * i)) & 3u) : hh);
-          }
-          *reinterpret_cast<uint4*>(p.k_out + o) = pack8(x);
+          *reinterpret_cast<uint4*>(p.k_out + o) = stand_for<kSplit>(hi, lo, [&](int i) { return m[i]; });
         }
       }
       if (p.v_out) {
         const uint32_t hi = rb[R::kVHi + (2 * sub) * kBlock + row] | (rb[R::kVHi + (2 * sub + 1) * kBlock + row] << 8);
         const uint32_t lo = kSplit ? *reinterpret_cast<const uint16_t*>(rb + R::kQ4VLo + row * R::kRow + 2 * sub) : 0u;
         const uint32_t m = *reinterpret_cast<const uint32_t*>(rb + R::kVMetaOff + (row * (D / kGroup) + sub / 4) * 4);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t hh = (hi >> (2 * i)) & 3u;
-          x[i] = stands_for(m, kSplit ? (hh << 2) | ((lo >> (2 * i)) & 3u) : hh);
-        }
-        *reinterpret_cast<uint4*>(p.v_out + o) = pack8(x);
+        *reinterpret_cast<uint4*>(p.v_out + o) = stand_for<kSplit>(hi, lo, [&](int) { return m; });
       }
     }
   }

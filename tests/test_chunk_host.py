@@ -97,8 +97,8 @@ def test_bad_rotary_is_refused(m, c):
     cfg, cells = _cfg(m, [Q4], 1, 1), _cells(m, 1)
     nan = float("nan")
     for kw in (dict(dim=8), dict(dim=72), dict(dim=144), dict(dim=0), dict(positions=0), dict(cos_sin=FAKE + 4),
-               dict(interleaved=2), dict(qw=FAKE + 2), dict(kw=FAKE + 2), dict(eps=-1e-6), dict(eps=nan),
-               dict(eps=float("inf"))):
+               dict(interleaved=2), dict(qw=FAKE + 2), dict(kw=FAKE + 2), dict(kw=FAKE, eps=-1e-6),
+               dict(kw=FAKE, eps=nan), dict(kw=FAKE, eps=0.0), dict(qw=FAKE, eps=float("inf"))):
         assert _norm_rope(m, c, rotary=_rotary(c, **kw)) == 1, kw
         assert _append(m, c, cfg, cells, rotary=_rotary(c, **kw)) == 1, kw
     assert _append(m, c, cfg, cells, rotary=None) == 1  # queries need a rotary
