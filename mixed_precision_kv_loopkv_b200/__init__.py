@@ -3,9 +3,10 @@
 LoopKV: Loop-Aware KV Cache Compression for Serving Looped Transformers
 (Abstract): per-(loop, layer) KV cells stored 4-bit (split high/low 2-bit
 planes), 2-bit, or as a reuse of the final loop's cell, executed by one fused
-decode kernel.  The CUDA library (libloopkv.so, C ABI in include/loopkv.h)
-does all the work; this package only marshals arguments and sequences the
-per-cell calls of a looped decode step.
+decode kernel.  The CUDA library (libloopkv.so, C ABI in include/loopkv.h
+and include/loopkv_chunk.h) does all the work; this package only marshals
+arguments and sequences the per-cell calls of a looped decode step or of a
+chunk of new tokens.
 """
 
 from .chunk import (  # noqa: F401
@@ -43,4 +44,4 @@ from .loopkv import (  # noqa: F401
     loopkv_status_string,
     mask_words,
 )
-from .step import LoopedDecodeStep, prefill  # noqa: F401
+from .step import LoopedChunkStep, LoopedDecodeStep, prefill  # noqa: F401

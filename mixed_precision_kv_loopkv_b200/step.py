@@ -15,12 +15,18 @@ position n:
     is passed to the kernel as one more, exact, token.
 The model's projections and MLPs are not part of this path; each cell's query
 and new K/V are given tensors.
+
+A prompt, a part of one or a few drafted tokens take the same order a chunk at
+a time (LoopedChunkStep): a stored cell norms, rotates and stores the chunk's
+keys and values and attends over what is stored; a reuse cell attends over the
+final loop's tokens of the earlier chunks and the chunk's own exact rows.
 """
 
 from __future__ import annotations
 
 import torch
 
+from .chunk import Rotary, loopkv_chunk_attention, loopkv_norm_rope, loopkv_rope_append
 from .loopkv import (LOOPKV_CELL_REUSE, KVCells, loopkv_append_decode_attention, loopkv_decode_attention,
                      loopkv_quantize_append)
 
@@ -119,3 +125,60 @@ class LoopedDecodeStep:
                 self.run()
                 self.advance()
         return g
+
+
+class LoopedChunkStep:
+    """A chunk of new tokens through every (loop, layer) cell, in order.
+
+    Two launches a cell: loopkv_rope_append (reuse cells: loopkv_norm_rope) and
+    loopkv_chunk_attention.
+
+    start   : device int32[B], stored tokens of every sequence (negative: the
+              sequence is skipped); ``advance()`` moves it by the chunk
+    lens    : device int32[B], the sequences' new tokens, or None (all T)
+    q, k, v : per cell, bf16 [B, T, H, D] and [B, T, Hkv, D] before norm and
+              rotation, strided views of a projection included
+    rotary  : a Rotary for all cells, or one for each layer
+    out     : per cell, bf16 [B, T, H, D] (written)
+    """
+
+    def __init__(self, kv: KVCells, block_table, start, q, k, v, out, rotary, sm_scale: float, lens=None,
+                 max_seq_len: int = 0, err_flag=None, cells=None):
+        self.kv, self.block_table, self.start, self.lens = kv, block_table, start, lens
+        self.q, self.k, self.v, self.out = q, k, v, out
+        self.rotary = [rotary] * kv.num_layers if isinstance(rotary, Rotary) else list(rotary)
+        if len(self.rotary) != kv.num_layers:
+            raise ValueError("one rotary for all layers or one for each")
+        self.sm_scale, self.max_seq_len, self.err_flag = sm_scale, max_seq_len, err_flag
+        self.cells = list(range(len(kv.plan_codes))) if cells is None else sorted(cells)
+        # rotated queries (and a reuse cell's keys): one cell's at a time
+        shapes = {"q": self.q[self.cells[0]].shape, "k": self.k[self.cells[0]].shape} if self.cells else {}
+        self._rows = {name: torch.zeros(shape, dtype=torch.bfloat16, device=start.device) for name, shape in shapes.items()}
+
+    def launches_per_step(self) -> int:
+        return 2 * len(self.cells)
+
+    def run(self, stream=None):
+        """Enqueue the chunk.  Not to be run twice at the same place without
+        ``advance()``: storing a chunk completes key groups whose exact keys the
+        chunk's own last tokens then replace."""
+        kv, qr = self.kv, self._rows.get("q")
+        for cell in self.cells:
+            loop, layer = divmod(cell, kv.num_layers)
+            args = dict(new_lens=self.lens, err_flag=self.err_flag, stream=stream)
+            if kv.plan_codes[cell] == LOOPKV_CELL_REUSE:
+                kr = self._rows["k"]
+                loopkv_norm_rope(self.rotary[layer], self.q[cell], self.k[cell], self.start, q_out=qr, k_out=kr, **args)
+                loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, self.start, sm_scale=self.sm_scale,
+                                       out=self.out[cell], max_seq_len=self.max_seq_len, k_cur=kr, v_cur=self.v[cell], **args)
+            else:
+                loopkv_rope_append(kv, loop, layer, self.rotary[layer], self.q[cell], self.k[cell], self.v[cell],
+                                   self.block_table, self.start, q_out=qr, **args)
+                loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, self.start, sm_scale=self.sm_scale,
+                                       out=self.out[cell], max_seq_len=self.max_seq_len, **args)
+
+    def advance(self):
+        if not self.cells:
+            return
+        new = self.q[self.cells[0]].shape[1] if self.lens is None else self.lens
+        self.start.add_((self.start >= 0) * new)

@@ -288,3 +288,304 @@ def test_chunk_attention_scales(m, kind, scale, v_scale):
 def test_chunk_attention_peaked(m):
     """Logits of some hundred: a single key has all the weight."""
     attention_case(m, "q4", 128, 2, 2, [300], [70], 70, False, seed=8, q_std=8.0)
+
+
+# ---------------------------------------------------------------- together, and on the edges of what is allowed
+
+
+def store(m, kind, B, hkv, d, capacity, heads, lens, seed=21):
+    kv, table = cell_for(m, kind, B, hkv, d, capacity, heads, seed=seed)
+    k, v = seeded_bf16((B, capacity, hkv, d), seed + 1), seeded_bf16((B, capacity, hkv, d), seed + 2)
+    m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0] * B), ints(lens))
+    return kv, table, k, v
+
+
+def expect_rows(kind, k, v, stored, q, starts, lens, sm_scale, cur=None):
+    """Oracle rows of every (sequence, head): [(b, h, rows, slack)]."""
+    g = q.shape[2] // k.shape[2]
+    found = []
+    for b, (s, n) in enumerate(zip(starts, lens)):
+        for j in range(k.shape[2]):
+            kh, vh = CO.stored_values(kind, host(k[b, :stored[b], j]), host(v[b, :stored[b], j]))
+            if cur is not None:
+                kh, vh = np.vstack([kh, host(cur[0][b, :n, j])]), np.vstack([vh, host(cur[1][b, :n, j])])
+            for h in range(j * g, (j + 1) * g):
+                found.append((b, h, *CO.chunk_attend(host(q[b, :n, h]), kh, vh, s + np.arange(n), sm_scale)))
+    return found
+
+
+def check_rows(out, found):
+    for b, h, want, slack in found:
+        assert np.all(np.abs(host(out[b, :want.shape[0], h]) - want) <= slack), (b, h)
+
+
+@pytest.mark.parametrize("hkv,heads", [(2, 2), (1, 4)])
+def test_looped_chunk_step(m, hkv, heads):
+    """Three ragged chunks through a plan of every kind: each cell's rows are the
+    oracle's, from its own rotated and stored (or exact) keys."""
+    L, N, B, d, cap = 2, 3, 3, 64, 260
+    plan = ["q4", "reuse", "reuse", "q2", "bf16", "q4"]
+    rng = np.random.default_rng(3)
+    mb = -(-cap // 16)
+    table = torch.from_numpy(rng.permutation(B * mb + 5)[: B * mb].reshape(B, mb).astype(np.int32)).cuda()
+    kv = m.KVCells(plan, L, N, heads, d, B * mb + 5, B, mb, num_kv_heads=hkv)
+    layers = [rotary_for(m, d, 64, False, True, seed=30 + 2 * j) for j in range(N)]
+    start, err = ints([0, 0, 0]), ints([0])
+    history = {c: [[], []] for c in range(6)}     # per cell: what the sequences' tokens are (k rotated, v)
+    have = [0] * B
+    T = 90
+    for step, lens in enumerate([[90, 33, 1], [64, 90, 70], [1, 7, 90]]):
+        rows = {c: fused_rows(B, T, heads, hkv, d, seed=1000 * step + c) for c in range(6)}
+        q, k, v = ({c: rows[c][i] for c in range(6)} for i in range(3))
+        out = {c: torch.zeros((B, T, heads, d), dtype=torch.bfloat16, device="cuda") for c in range(6)}
+        chunk = m.LoopedChunkStep(kv, table, start, q, k, v, out, [x[0] for x in layers], 0.2, lens=ints(lens), err_flag=err)
+        assert chunk.launches_per_step() == 12
+        chunk.run()
+        assert int(err) == 0
+        turned = {}
+        for c in range(6):
+            _, qa, ka = layers[c % N]
+            turned[c] = [[CO.norm_rope(host(x[c][b, :n]), have[b] + np.arange(n), **a) for b, n in enumerate(lens)]
+                         for x, a in ((q, qa), (k, ka))]
+        before = {c: [list(x) for x in history[c]] for c in range(6)}
+        for c in range(6):
+            history[c][0].append(turned[c][1])
+            history[c][1].append([host(v[c][b, :n]) for b, n in enumerate(lens)])
+        for c in range(6):
+            src = c + 3 if plan[c] == "reuse" else c
+            kept = before[src] if plan[c] == "reuse" else history[src]
+            for b, n in enumerate(lens):
+                kk, vv = (np.concatenate([x[b] for x in part] + [np.zeros((0, hkv, d), np.float32)]) for part in kept)
+                for h in range(heads):
+                    j = h * hkv // heads
+                    kh, vh = CO.stored_values(plan[src], kk[:, j], vv[:, j])
+                    if plan[c] == "reuse":
+                        kh = np.vstack([kh, turned[c][1][b][:, j]])
+                        vh = np.vstack([vh, host(v[c][b, :n, j])])
+                    want, slack = CO.chunk_attend(turned[c][0][b][:, h], kh, vh, have[b] + np.arange(n), 0.2)
+                    assert np.all(np.abs(host(out[c][b, :n, h]) - want) <= slack), (step, c, b, h)
+        chunk.advance()
+        have = [a + n for a, n in zip(have, lens)]
+        assert start.tolist() == have
+
+
+def test_chunk_then_decode_step(m):
+    """The prompt side feeds the decode step: after a chunk, a decode step's
+    stored cell attends over chunk and new token (checked against a chunk of one)."""
+    B, H, d = 2, 4, 128
+    kv, table, k, v = store(m, "q4", B, H, d, 100, H, [77, 64])
+    q, kn, vn = (seeded_bf16((B, 1, H, d), 50 + i, 0.2) for i in range(3))
+    start = ints([77, 64])
+    m.loopkv_rope_append(kv, 0, 0, None, None, kn, vn, table, start)
+    one = m.loopkv_chunk_attention(kv, 0, 0, q, table, start, sm_scale=0.5)
+    dec = m.loopkv_decode_attention(kv, 0, 0, q[:, 0].contiguous(), table, start + 1, tau=0.0, sm_scale=0.5)
+    full = [torch.cat([x, torch.zeros_like(x[:, :1])], 1) for x in (k, v)]
+    for b, n in enumerate([77, 64]):
+        full[0][b, n], full[1][b, n] = kn[b, 0], vn[b, 0]
+    found = expect_rows("q4", *full, [78, 65], q, [77, 64], [1, 1], 0.5)
+    check_rows(one, found)
+    check_rows(dec[:, None], found)
+
+
+@pytest.mark.parametrize("kind", ["q4", "bf16"])
+@pytest.mark.parametrize("T", [3, 140])
+def test_chunk_attention_device_faults(m, kind, T):
+    """A bad block, a length beyond the bound and bad counts answer with zeros (or
+    nothing) and a flag; the other sequences are as without them."""
+    B, H, d, cap = 5, 2, 64, 400
+    lens, starts = [T] * B, [200, 100, 250, 0, 31]
+    kv, table, k, v = store(m, kind, B, H, d, cap, H, [s + T for s in starts])
+    q = seeded_bf16((B, T, H, d), 9, 0.3)
+    good = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints(starts), ints(lens))
+    bad = table.clone()
+    bad[1, 2], bad[4, 0] = kv.num_blocks, -1
+    err = ints([0])
+    out = torch.full_like(good, 7.0)
+    m.loopkv_chunk_attention(kv, 0, 0, q, bad, ints(starts), ints([T, T, T, T + 1, T]), out=out, err_flag=err)
+    assert int(err) == m.LOOPKV_DEVERR_BLOCK_ID | m.LOOPKV_DEVERR_SEQ_LEN
+    assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    assert not out[1].any() and not out[4].any() and (out[3] == 7).all()
+    err.zero_()
+    # the bound also sizes the split of the context, so the same bits are those of the same bound
+    ok = [s + T <= 249 for s in starts]
+    good = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([s if f else -1 for s, f in zip(starts, ok)]), ints(lens),
+                                    max_seq_len=249, err_flag=err)
+    assert int(err) == 0 and not all(ok)
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints(starts), ints(lens), max_seq_len=249, err_flag=err)
+    assert int(err) == m.LOOPKV_DEVERR_SEQ_LEN
+    for b in range(B):
+        assert torch.equal(out[b], good[b]) and bool(out[b].any()) == ok[b]
+
+
+@pytest.mark.parametrize("kind,T", [("q4", 2), ("q2", 2), ("q4", 70)])
+def test_chunk_attention_ignores_what_is_not_there(m, kind, T):
+    """Stored bytes behind the last token, the open group's stale planes and the
+    rows behind a chunk may hold anything, NaN included."""
+    B, H, d, cap = 3, 2, 128, 160
+    starts = [40, 64, 7]
+    lens = [T, max(1, T - 1), 1]
+    stored = [s + n for s, n in zip(starts, lens)]
+    kv, table, k, v = store(m, kind, B, H, d, cap, H, stored)
+    q = seeded_bf16((B, T, H, d), 9, 0.3)
+    good = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints(starts), ints(lens))
+    arena = kv.arena_view(0)
+    before = arena.clone()
+    ref, _, _, _ = store(m, kind, B, H, d, cap, H, stored)      # the bytes that are meant, over 0xFF elsewhere
+    ref.arenas[0].fill_(0xFF)
+    m.loopkv_rope_append(ref, 0, 0, None, None, k, v, table, ints([0] * B), ints(stored))
+    arena.copy_(ref.arena_view(0))
+    for b in range(B):
+        kv.residuals[0][b, :, stored[b] % 32:] = float("nan")
+        q[b, lens[b]:] = float("nan")
+    assert not torch.equal(before, arena)
+    again = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints(starts), ints(lens))
+    assert torch.equal(again, good)
+    got = m.loopkv_read_tokens(kv, 0, 0, table, ints(stored), ints([0] * B), cap)
+    assert not torch.isnan(got[0]).any() and not torch.isnan(got[1]).any()
+
+
+def test_shared_blocks_and_a_repeated_block(m):
+    """Two sequences on the same blocks (a shared prefix), and one whose table
+    names a block twice, are read as they are."""
+    H, d = 2, 128
+    kv, table, k, v = store(m, "q4", 2, H, d, 128, H, [128, 128])
+    shared = table.clone()
+    shared[1] = shared[0]
+    q = seeded_bf16((2, 4, H, d), 3, 0.2)
+    q[1] = q[0]
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, shared, ints([124, 124]))
+    assert torch.equal(out[0], out[1])
+    shared[1, 4:6] = shared[1, 0:2]          # keys 64 .. 95 are keys 0 .. 31 again
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, shared, ints([124, 124]))
+    kk, vv = (torch.cat([x[0:1, :64], x[0:1, :32], x[0:1, 96:]], 1) for x in (k, v))
+    check_rows(out[1:], expect_rows("q4", kk, vv, [128], q[1:], [124], [4], 1.0))
+
+
+def test_calls_on_two_streams_at_once(m):
+    """The same cell read by two streams while each has its own output, and two
+    cells appended to at once."""
+    B, H, d = 2, 4, 128
+    kv, table, k, v = store(m, "q4", B, H, d, 600, H, [600, 555])
+    other, _ = cell_for(m, "q4", B, H, d, 600, H)
+    q = [seeded_bf16((B, T, H, d), T, 0.2) for T in (4, 200)]
+    start = [ints([596, 551]), ints([400, 355])]
+    want = [m.loopkv_chunk_attention(kv, 0, 0, x, table, s) for x, s in zip(q, start)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [[torch.empty_like(w) for _ in range(10)] for w in want]
+    for i in range(10):
+        for j in range(2):
+            m.loopkv_chunk_attention(kv, 0, 0, q[j], table, start[j], out=outs[j][i], stream=streams[j])
+    m.loopkv_rope_append(other, 0, 0, None, None, k, v, table, ints([0, 0]), ints([600, 555]), stream=streams[2])
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(o, want[j]) for o in outs[j])
+    same_cell(other, kv, [600, 555])
+
+
+def test_captured_and_replayed_with_new_positions(m):
+    """A captured pair of calls replays with the positions, lengths and rows that
+    its buffers then hold."""
+    B, H, d, T = 2, 2, 64, 5
+    kv, table, k, v = store(m, "q4", B, H, d, 200, H, [0, 0])
+    ref, _, _, _ = store(m, "q4", B, H, d, 200, H, [0, 0])
+    r, _, _ = rotary_for(m, d, 64, True, True)
+    q, kn, vn = (torch.zeros(B, T, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    start, lens, err = ints([-1, -1]), ints([T, T]), ints([0])
+    qr, out = torch.zeros_like(q), torch.zeros_like(q)
+
+    def both(cell, qr, out):
+        m.loopkv_rope_append(cell, 0, 0, r, q, kn, vn, table, start, lens, qr, err_flag=err)
+        m.loopkv_chunk_attention(cell, 0, 0, qr, table, start, lens, 0.3, out, err_flag=err)
+
+    both(kv, qr, out)                        # skipped sequences: nothing is stored
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(kv, qr, out)
+    have = [0, 0]
+    for i in range(12):
+        n = [1 + i % T, T - i % 3]
+        for j, x in enumerate((q, kn, vn)):
+            x.copy_(seeded_bf16((B, T, H, d), 100 * i + j))
+        start.copy_(ints(have))
+        lens.copy_(ints(n))
+        graph.replay()
+        qr2, out2 = torch.zeros_like(q), torch.zeros_like(q)
+        both(ref, qr2, out2)
+        for b in range(2):
+            assert torch.equal(out[b, :n[b]], out2[b, :n[b]])
+        have = [a + c for a, c in zip(have, n)]
+        same_cell(kv, ref, have)
+    assert int(err) == 0
+
+
+def test_binding_refusals(m):
+    kv, table, k, v = store(m, "q4", 2, 2, 64, 64, 2, [10, 10])
+    q = seeded_bf16((2, 3, 2, 64), 1)
+    s, r = ints([7, 7]), m.Rotary()
+    ok = lambda **kw: m.loopkv_chunk_attention(kv, 0, 0, kw.pop("q", q), kw.pop("table", table), kw.pop("s", s), **kw)  # noqa: E731
+    ok()
+    for kw, text in ((dict(q=q.float()), "bfloat16"), (dict(q=q[:, :, :1]), "shape"), (dict(q=q.transpose(2, 3)), "shape"),
+                     (dict(s=s.long()), "int32"), (dict(s=s[:1]), "shape"), (dict(table=table[:, :2]), "shape"),
+                     (dict(out=q), "overlaps q"), (dict(k_cur=q), "together"), (dict(out=torch.empty_like(q).transpose(1, 2)), "out"),
+                     (dict(q=seeded_bf16((2, 3, 2, 65), 1)[..., 1:]), "multiples of 8"), (dict(new_lens=s.cpu()), "CUDA")):
+        with pytest.raises(ValueError, match=text):
+            ok(**kw)
+    with pytest.raises(m.LoopKVError):
+        ok(max_seq_len=65)
+    with pytest.raises(ValueError, match="overlaps k_new"):
+        m.loopkv_rope_append(kv, 0, 0, r, q, q, v[:, :3], table, s, q_out=q)
+    with pytest.raises(ValueError, match="rotary"):
+        m.loopkv_rope_append(kv, 0, 0, None, q, k[:, :3], v[:, :3], table, s)
+    with pytest.raises(ValueError, match="entries"):
+        m.loopkv_norm_rope(m.Rotary(q_weight=seeded_bf16((128,), 1)), q, None, s)
+    with pytest.raises(ValueError, match="overlaps"):
+        m.loopkv_read_tokens(kv, 0, 0, table, s, s, 3, k_out=q, v_out=q)
+    with pytest.raises(ValueError, match="no cell"):
+        m.loopkv_read_tokens(kv, 1, 0, table, s, s, 3)
+    with pytest.raises(ValueError, match="no storage"):
+        m.loopkv_read_tokens(m.KVCells(["q4", "q4"], 1, 2, 2, 64, 8, 2, 4, allocate={0}), 0, 1, table, s, s, 3)
+
+
+def test_empty_chunks(m):
+    kv, table, k, v = store(m, "q4", 2, 2, 64, 64, 2, [10, 10])
+    q, s = seeded_bf16((2, 0, 2, 64), 1), ints([10, 10])
+    assert m.loopkv_chunk_attention(kv, 0, 0, q, table, s).shape == q.shape
+    m.loopkv_rope_append(kv, 0, 0, m.Rotary(), q, q, q, table, s)
+    assert m.loopkv_norm_rope(m.Rotary(), q, q, s)[1].shape == q.shape
+    assert m.loopkv_read_tokens(kv, 0, 0, table, s, s, 0)[0].shape == q.shape
+    none = ints([])
+    x = seeded_bf16((0, 4, 2, 64), 1)
+    assert m.loopkv_chunk_attention(kv, 0, 0, x, table[:0], none).shape == x.shape
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2"])
+def test_long_context(m, kind):
+    """Context longer than the decode kernel's limit, and offsets into an arena
+    of more than 2^31 bytes."""
+    d, n, T = 128, 70_000, 3
+    rec = m.loopkv_record_bytes(d, kind)
+    pool = 2**31 // rec + 6000
+    mb = -(-n // 16)
+    kv = m.KVCells([kind], 1, 1, 1, d, pool, 1, mb)
+    table = torch.arange(pool - 1, pool - 1 - mb, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    k, v = seeded_bf16((1, n, 1, d), 1), seeded_bf16((1, n, 1, d), 2)
+    m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0]))
+    q = seeded_bf16((1, T, 1, d), 3, 0.4)
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([n - T]))
+    check_rows(out, expect_rows(kind, k, v, [n], q, [n - T], [T], 1.0))
+    wide = seeded_bf16((1, 150, 1, d), 4, 0.4)
+    out = m.loopkv_chunk_attention(kv, 0, 0, wide, table, ints([n - 150]))
+    check_rows(out[:, ::37], [(b, h, w[::37], e[::37]) for b, h, w, e in
+                              expect_rows(kind, k, v, [n], wide, [n - 150], [150], 1.0)])
+
+
+def test_zero_and_negative_scales(m):
+    """sm_scale 0 weighs all visible keys alike; a negative one turns the order."""
+    B, H, d = 1, 2, 64
+    kv, table, k, v = store(m, "q4", B, H, d, 100, H, [100])
+    for T in (2, 40):
+        q = seeded_bf16((B, T, H, d), 5)
+        for sm in (0.0, -0.4):
+            out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([100 - T]), sm_scale=sm)
+            check_rows(out, expect_rows("q4", k, v, [100], q, [100 - T], [T], sm))
