@@ -732,9 +732,10 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     int v_ref = -1000;
     for (int h = 0; h < steps && ok; ++h) {
       const int j = h >> 1, buf = h & 1, gt = job.tile0 + j;
-      // the tile's exponents come with its keys and values
-      ok = (buf || (warp_wait(k_full(j & 1), (j >> 1) & 1) && warp_wait(v_full(j & 1), (j >> 1) & 1))) &&
-           warp_wait(s_full(m), h & 1);
+      // The tile's exponents come with its values (its keys came before).  The
+      // logits' arrival tells that all products issued before theirs are done,
+      // those of two steps ago among them, which read the weights' buffer.
+      ok = (buf || warp_wait(v_full(j & 1), (j >> 1) & 1)) && warp_wait(s_full(m), h & 1);
       if (!ok) break;
       if (idle) {
         if (lane == 0) {
@@ -805,8 +806,6 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
         m_ref = m_new;
         v_ref = v_new;
       }
-      // the weights' buffer: the products of two steps ago have read it
-      if (h >= 2) ok = ok && warp_wait(o_done(m, buf), ((h >> 1) - 1) & 1);
       const float base = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
