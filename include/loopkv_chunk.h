@@ -132,14 +132,18 @@ LOOPKV_API loopkv_status loopkv_read_tokens(const loopkv_config* cfg, const loop
  * share one read of the low value plane, so the threshold tau of single-token
  * decoding has nothing to save here (as tau = 0 there).  Softmax weights and
  * dequantised rows enter the tensor cores in fp16 (11 bits) under powers of two
- * that follow the data, sums and statistics are fp32.
+ * that follow the data, a block of 16 (or group of 32) tokens at a time; sums
+ * and statistics are fp32.  Entries less than 2^-8 of the largest of their
+ * block lose bits by the same factor (exact keys, and bf16 cells: 2^-22).
  *   q            : rows of num_heads heads (queries already rotated)
  *   k_cur, v_cur : optional rows of num_kv_heads heads (both or neither)
  *   max_seq_len  : host upper bound of the stored tokens; 0: the block table's
- *                  capacity
+ *                  capacity.  It sizes the split of the context: results under
+ *                  different bounds may differ in their last bits
  *   out          : device bf16 [batch][num_tokens][num_heads][D]; rows of a
- *                  sequence skipped by start_pos[b] < 0 or by a device fault are
- *                  zeros up to new_lens[b] (nothing where that is out of range)
+ *                  sequence skipped by start_pos[b] < 0 or by a device fault (any
+ *                  bad block of it) are zeros up to new_lens[b] (nothing where
+ *                  that is out of range)
  * Errors: INVALID_ARG as for loopkv_decode_attention and loopkv_rows; BAD_PLAN;
  * UNSUPPORTED for 2^31 rows or more.
  */

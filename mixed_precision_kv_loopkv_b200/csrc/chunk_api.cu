@@ -10,7 +10,8 @@ namespace {
 
 using namespace loopkv;
 
-constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;  // and tokens of a sequence
+constexpr float kLog2e = 1.4426950408889634f;
 
 bool rows_ok(const loopkv_rows* r) {
   return r->data && aligned16(r->data) && r->batch_stride >= 0 && r->token_stride >= 0 && r->head_stride >= 0 &&
@@ -130,7 +131,7 @@ loopkv_status loopkv_rope_append(const loopkv_config* cfg, const loopkv_cells* c
   p.key_blocks = static_cast<int>((int64_t{num_tokens} + 30) / 32 + 1);
   const int64_t cap_groups = (capacity(cfg) + 31) / 32;
   if (p.key_blocks > cap_groups) p.key_blocks = static_cast<int>(cap_groups);
-  if (static_cast<double>(batch) * num_tokens * cfg->num_heads > static_cast<double>(kMaxRows) ||
+  if (capacity(cfg) > kMaxRows || static_cast<double>(batch) * num_tokens * cfg->num_heads > static_cast<double>(kMaxRows) ||
       static_cast<double>(batch) * p.key_blocks * p.Hkv > static_cast<double>(kMaxRows / 2))
     return LOOPKV_ERR_UNSUPPORTED;
   return result(launch_rope_append(kind, cfg->head_dim, p, static_cast<cudaStream_t>(stream)));
@@ -170,7 +171,7 @@ loopkv_status loopkv_read_tokens(const loopkv_config* cfg, const loopkv_cells* c
   p.groups = static_cast<int>((int64_t{num_tokens} + 30) / 32 + 1);
   const int64_t cap_groups = (capacity(cfg) + 31) / 32;
   if (p.groups > cap_groups) p.groups = static_cast<int>(cap_groups);
-  if (static_cast<double>(batch) * p.groups * p.Hkv > static_cast<double>(kMaxRows)) return LOOPKV_ERR_UNSUPPORTED;
+  if (capacity(cfg) > kMaxRows || static_cast<double>(batch) * p.groups * p.Hkv > static_cast<double>(kMaxRows)) return LOOPKV_ERR_UNSUPPORTED;
   return result(launch_read(cfg->plan[cell], cfg->head_dim, p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -184,7 +185,7 @@ loopkv_status loopkv_chunk_attention(const loopkv_config* cfg, const loopkv_cell
   int cell;
   if ((st = cell_index(cfg, loop, layer, &cell)) != LOOPKV_OK) return st;
   cell = source_cell(cfg, cell);
-  if (batch < 0 || batch > cfg->max_batch || num_tokens < 0 || !isfinite(sm_scale)) return LOOPKV_ERR_INVALID_ARG;
+  if (batch < 0 || batch > cfg->max_batch || num_tokens < 0 || !isfinite(sm_scale * kLog2e)) return LOOPKV_ERR_INVALID_ARG;
   if (max_seq_len < 0 || max_seq_len > capacity(cfg)) return LOOPKV_ERR_INVALID_ARG;
   if ((k_cur == nullptr) != (v_cur == nullptr)) return LOOPKV_ERR_INVALID_ARG;  // both or neither
   if (!cells || !cells->arena || !cells->key_residual) return LOOPKV_ERR_INVALID_ARG;
@@ -212,7 +213,7 @@ loopkv_status loopkv_chunk_attention(const loopkv_config* cfg, const loopkv_cell
   p.g_log2 = group == 8 ? 3 : group == 4 ? 2 : group == 2 ? 1 : 0;
   p.max_blocks = cfg->max_blocks_per_seq;
   p.num_blocks = cfg->num_blocks;
-  p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  p.sm_scale_log2 = sm_scale * kLog2e;
   return result(launch_chunk_attention(cfg->plan[cell], cfg->head_dim, p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -190,7 +190,7 @@ struct FewWarp {
           top = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(top, w.x), w.y), w.z), w.w);
         }
     }
-    const int e = block_exp(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
+    const int e = block_exp<kExactTopExp>(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
     const float f = pow2f(-e);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {

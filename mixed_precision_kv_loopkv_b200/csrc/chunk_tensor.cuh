@@ -13,6 +13,7 @@ constexpr int kTileKeys = 128;                       // keys of one tile: eight 
 constexpr int kStepKeys = 64;                        // keys of one step of products and softmax
 constexpr int kBlockWarps = kTileKeys / kBlock;      // dequantising warps, a block each
 constexpr int kExpRing = 4;
+constexpr int kPolyPair = 3;                         // of four pairs of weights, the one worked out on the FMA units
 
 // A block's keys (values) are stored as x 2^-e with e such that the largest is
 // in [2^-7, 2^-6): then 2^24 times a 4-bit scale, at most 2^24 (2 2^-6 / 15)
@@ -46,12 +47,12 @@ __host__ __device__ constexpr int chunk_threads() { return (MT * 4 + kBlockWarps
 
 // Registers a thread after the split.  They come out of what the block was
 // launched with, 65536 / threads rounded down to a multiple of 8 a thread:
-// MT = 2: 5 groups of 96 >= 2 x 136 + 2 x 80 + 48.  MT = 1: 4 of 128 each, as launched.
+// MT = 2: 5 groups of 96 >= 2 x 128 + 2 x 88 + 48.  MT = 1: 4 of 128 each, as launched.
 template <int MT>
 struct ChunkRegs {
-  static constexpr int kSoftmax = MT == 2 ? 136 : 128, kDequant = MT == 2 ? 80 : 128, kIssue = MT == 2 ? 48 : 128;
+  static constexpr int kSoftmax = 128, kDequant = MT == 2 ? 88 : 128, kIssue = MT == 2 ? 48 : 128;
   static constexpr int kLaunch = 65536 / chunk_threads<MT>() / 8 * 8;
-  static constexpr bool kMoves = kSoftmax != kLaunch;
+  static constexpr bool kMoves = MT == 2;
   static_assert(MT * kSoftmax + 2 * kDequant + kIssue <= (MT + 3) * kLaunch, "register split");
 };
 
@@ -64,9 +65,15 @@ __device__ __forceinline__ float pow2f(int e) {
 }
 
 // Exponent e of a block whose largest absolute value has the float bits u:
-// the value times 2^-e is in [2^-7, 2^-6) (smaller where e is held at -100).
+// the value times 2^-e is in [2^(TOP - 1), 2^TOP) (smaller where e is held at
+// -100).  Exact rows have no codes to make room for: their keys, and a bf16
+// cell's values, stand at 2^8, which leaves entries 2^-22 of the largest whole.
+// Exact values beside quantised ones keep to the place of those, since one
+// exponent serves the outputs of both.
+constexpr int kExactTopExp = 8;
+template <int TOP = kTopExp>
 __device__ __forceinline__ int block_exp(uint32_t abs_bits) {
-  return max(static_cast<int>(abs_bits >> 23) - 127 - kTopExp + 1, -100);
+  return max(static_cast<int>(abs_bits >> 23) - 127 - TOP + 1, -100);
 }
 
 // The upper two bits of each nibble from hi, the lower two from lo: one
@@ -153,6 +160,26 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// 2^x of two numbers x <= 100 on the FMA units: x = n + f with n the nearest
+// integer (added to 1.5 2^23 and taken off again) and |f| <= 1/2, a cubic for
+// 2^f (fitted at Chebyshev nodes to the least relative error, 7.5e-5, a third of
+// what rounding a weight to fp16 may add), n into the exponent.  -inf and all
+// below -126 give 2^-126, which is 0 as a weight.
+__device__ __forceinline__ void poly_exp2(uint64_t x2, float& a, float& b) {
+  unpack2(x2, a, b);
+  const uint64_t x = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const uint64_t n = add2(x, pack2(12582912.f, 12582912.f));
+  const uint64_t f = fma2(add2(n, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), x);
+  uint64_t y = fma2(f, pack2(5.517158285e-02f, 5.517158285e-02f), pack2(2.426111102e-01f, 2.426111102e-01f));
+  y = fma2(y, f, pack2(6.932610273e-01f, 6.932610273e-01f));
+  y = fma2(y, f, pack2(9.999280572e-01f, 9.999280572e-01f));
+  float na, nb;
+  unpack2(n, na, nb);
+  unpack2(y, a, b);
+  a = __int_as_float(__float_as_int(a) + (__float_as_int(na) << 23));
+  b = __int_as_float(__float_as_int(b) + (__float_as_int(nb) << 23));
 }
 
 // Bounded wait of a whole warp; the same answer for all its threads.
@@ -389,7 +416,7 @@ struct BlockLoader {
         top = abs_max_bf16x2(abs_max_bf16x2(top, w[k][j].z), w[k][j].w);
       }
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-    const int e = block_exp(top << 16);
+    const int e = block_exp<KEYS || !kQuant ? kExactTopExp : kTopExp>(top << 16);
     const float f = pow2f(-e);
 #pragma unroll
     for (int k = 0; k < KPL; ++k) {
@@ -817,8 +844,13 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float x, y;
-          unpack2(fma2(pack2(__uint_as_float(r[16 * c + 2 * i]), __uint_as_float(r[16 * c + 2 * i + 1])), f2, off2), x, y);
-          x = fast_exp2(x), y = fast_exp2(y);
+          const uint64_t e = fma2(pack2(__uint_as_float(r[16 * c + 2 * i]), __uint_as_float(r[16 * c + 2 * i + 1])), f2, off2);
+          if (i % 4 == kPolyPair) {
+            poly_exp2(e, x, y);
+          } else {
+            unpack2(e, x, y);
+            x = fast_exp2(x), y = fast_exp2(y);
+          }
           part = add2(part, pack2(x, y));
           w[i] = half2_bits(__floats2half2_rn(x, y));
         }

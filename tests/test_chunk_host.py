@@ -218,3 +218,12 @@ def test_oracle_chunk_of_one_is_decode():
         assert np.max(np.abs(got[0] - want)) < 1e-12 and np.all(slack > 0)
     empty, _ = CO.chunk_attend(q[None], k[:0], v[:0], [-1], 1.0)
     assert not empty.any()
+
+
+def test_capacity_beyond_31_bits_is_unsupported(m, c):
+    cfg, cells = _cfg(m, [Q4], 1, 1, max_blocks_per_seq=1 << 27), _cells(m, 1)
+    assert _append(m, c, cfg, cells) == 3 and _read(m, cfg, cells) == 3 and _attend(m, c, cfg, cells) == 3
+
+
+def test_scale_that_overflows_is_invalid(m, c):
+    assert _attend(m, c, _cfg(m, [Q4], 1, 1), _cells(m, 1), sm_scale=3e38) == 1

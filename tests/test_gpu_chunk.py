@@ -589,3 +589,35 @@ def test_zero_and_negative_scales(m):
         for sm in (0.0, -0.4):
             out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([100 - T]), sm_scale=sm)
             check_rows(out, expect_rows("q4", k, v, [100], q, [100 - T], [T], sm))
+
+
+@pytest.mark.parametrize("kind", ["q4", "bf16"])
+@pytest.mark.parametrize("T", [3, 150])
+def test_rows_behind_a_current_chunk_are_not_read(m, kind, T):
+    B, H, d = 2, 2, 128
+    kv, table, k, v = store(m, kind, B, H, d, 64, H, [50, 0])
+    q, kc, vc = (seeded_bf16((B, T, H, d), 60 + i, 0.4) for i in range(3))
+    start, lens = ints([50, 0]), ints([T - 1, 2])
+    good = m.loopkv_chunk_attention(kv, 0, 0, q, table, start, lens, k_cur=kc, v_cur=vc)
+    for x in (q, kc, vc):
+        for b, n in enumerate([T - 1, 2]):
+            x[b, n:] = float("nan")
+    again = m.loopkv_chunk_attention(kv, 0, 0, q, table, start, lens, k_cur=kc, v_cur=vc)
+    assert torch.equal(good, again) and not torch.isnan(again).any()
+
+
+@pytest.mark.parametrize("T", [5, 140])
+def test_outlier_channels_of_exact_keys(m, T):
+    """Keys with a channel 2^12 times the others, as open groups, bf16 cells and
+    current rows hold them exactly: the logits keep the small channels whole."""
+    B, H, d, n = 1, 2, 64, 100
+    kv, table = cell_for(m, "bf16", B, H, d, n)
+    k, v = seeded_bf16((B, n, H, d), 1), seeded_bf16((B, n, H, d), 2)
+    kc, vc = seeded_bf16((B, T, H, d), 3), seeded_bf16((B, T, H, d), 4)
+    q = seeded_bf16((B, T, H, d), 5, 0.3)
+    k[..., 7] *= 4096
+    kc[..., 7] *= 4096
+    q[..., 7] *= 2.0**-12
+    m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0]))
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([n]), k_cur=kc, v_cur=vc)
+    check_rows(out, expect_rows("bf16", k, v, [n], q, [n], [T], 1.0, cur=(kc, vc)))
