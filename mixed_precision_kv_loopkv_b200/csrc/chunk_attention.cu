@@ -53,7 +53,7 @@ cudaError_t launch_clusters(Kernel kern, int64_t units, int splits, int threads,
   return cudaLaunchKernelEx(&cfg, kern, p, args..., splits);
 }
 
-// Shared-memory limit of a kernel (MT = 0: the one for few rows), once a device;
+// Shared-memory limit of a kernel (MT < 0: of -MT warps, for few rows), once a device;
 // regs: registers that it must have been built with (0: any).
 template <int KIND, int D, int MT, typename Kernel>
 cudaError_t prepare_once(Kernel kern, size_t smem, int regs, int dev) {
@@ -92,25 +92,43 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
   return launch_clusters(kern, units, splits, chunk_threads<MT>(), kSmem, stream, p, static_cast<int>(row_tiles));
 }
 
-// Few rows: the split with the fewest group times on the busiest SM, a CTA's
-// start and join counted as two.
+template <int KIND, int D, int WARPS>
+cudaError_t launch_few_w(const ChunkAttnParams& p, int64_t units, int splits, int dev, cudaStream_t stream) {
+  using L = FewSmem<KIND, D, WARPS>;
+  static_assert(kFewWarpsPerSm / WARPS * (L::kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
+  static constexpr auto kern = chunk_few_kernel<KIND, D, WARPS>;
+  const cudaError_t e = prepare_once<KIND, D, -WARPS>(kern, L::kBytes, 0, dev);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(kern, units, splits, WARPS * 32, L::kBytes, stream, p);
+}
+
+// Few rows: the CTA size and split of least estimated time, in the time that an
+// SM with twelve warps at work takes a 32-token group (440 cycles): what the
+// busiest SM has to read, or six for each group that a warp takes one after
+// another; and for each wave of CTAs their start and end, 25, or 55 as clusters.
+// Measured, 512 (sequence, head) pairs of 4100 tokens: CTAs of 12 warps 144 us,
+// of 6 warps 130, of 3 warps 122 (one wave), of 3 warps in clusters of two 131.
+// With 16 pairs of 16384 tokens, 12 warps in clusters of eight put every SM to work.
 template <int KIND, int D>
 cudaError_t launch_few(const ChunkAttnParams& p, cudaStream_t stream) {
-  using L = FewSmem<KIND, D>;
-  static_assert(L::kBytes <= 227 * 1024, "shared memory of one CTA");
   const int dev = current_device();
-  static constexpr auto kern = chunk_few_kernel<KIND, D>;
-  const cudaError_t e = prepare_once<KIND, D, 0>(kern, L::kBytes, 0, dev);
-  if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(p.Hkv) * p.chunk.B, sms = sm_count(dev);
   const int64_t groups = (static_cast<int64_t>(p.max_stored) + kGroup - 1) / kGroup + (p.k_cur.p ? 1 : 0);
-  int splits = 1;
+  auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  int splits = 1, warps = kFewWarpsPerSm;
   int64_t best = INT64_MAX;
-  for (int s = 1; s <= kMaxSplits; s *= 2) {
-    const int64_t cost = (units * s + sms - 1) / sms * ((groups + s * kFewWarps - 1) / (s * kFewWarps) + 2);
-    if (cost < best) best = cost, splits = s;
+  for (int w = kFewWarpsPerSm; w >= 3; w /= 2)
+    for (int s = 1; s <= kMaxSplits; s *= 2) {
+      const int64_t waves = ceil_div(units * s, sms * (kFewWarpsPerSm / w));
+      const int64_t busiest = ceil_div(units * s, sms) * ceil_div(groups, s), serial = waves * ceil_div(groups, s * w) * 6;
+      const int64_t cost = (busiest > serial ? busiest : serial) + waves * (s == 1 ? 25 : 55);
+      if (cost < best) best = cost, splits = s, warps = w;
+    }
+  switch (warps) {
+    case 3: return launch_few_w<KIND, D, 3>(p, units, splits, dev, stream);
+    case 6: return launch_few_w<KIND, D, 6>(p, units, splits, dev, stream);
+    default: return launch_few_w<KIND, D, 12>(p, units, splits, dev, stream);
   }
-  return launch_clusters(kern, units, splits, kFewWarps * 32, L::kBytes, stream, p);
 }
 
 template <int KIND, int D>

@@ -5,10 +5,15 @@
 // once, by bulk copies into its own ring in shared memory, and dequantises them
 // straight into the operand registers of 16 x 8 x 16 products: no tile is
 // written back.  (The 128-row products of chunk_tensor.cuh would spend more on
-// empty rows than the copy takes: 311 us against 153 for four tokens of 32
-// sequences over 4096 4-bit tokens and 16 heads.)  Twelve warps of a CTA take
-// every twelfth group, the CTAs of a cluster their share of the context; all
-// join through shared memory at the end.
+// empty rows than the copy takes.)  Each warp of a CTA takes every so-many-th
+// group, the CTAs of a cluster their share of the context; all join through
+// shared memory at the end.
+//
+// Measured on a B200, four tokens of 32 sequences over 4096 4-bit tokens and 16
+// heads of 128 (337 MB): 122 us, 2.8 TB/s, 42 % of measured; the 128-row kernel
+// 311 us.  Bound by instruction issue and its latencies (1035 a group, half of
+// the issue slots used with 12 warps an SM: the outputs and queries alone are 96
+// registers); 16 warps with the queries in shared memory spill: 10 % slower.
 //
 // Operand layout.  A product's columns (keys, or channels) are the eight
 // thread quads, its depth two pairs for each thread r of a quad.
@@ -25,19 +30,20 @@
 
 namespace loopkv {
 
-constexpr int kFewRows = 16, kFewWarps = 12, kFewStages = 3;
+constexpr int kFewRows = 16, kFewStages = 3, kFewWarpsPerSm = 12;
 
-template <int KIND, int D>
+// WARPS of a CTA: 3, 6 or 12, with 168 registers a thread always twelve an SM.
+template <int KIND, int D, int WARPS>
 struct FewSmem {
   static constexpr int kGroupBytes = 2 * Rec<KIND, D>::kBytes;
-  static constexpr int kRing = kFewWarps * kFewStages * kGroupBytes;
-  static constexpr int kOut = kFewWarps * kFewRows * D * 4;          // the warps' partial outputs, over the ring
+  static constexpr int kRing = WARPS * kFewStages * kGroupBytes;
+  static constexpr int kOut = WARPS * kFewRows * D * 4;          // the warps' partial outputs, over the ring
   static constexpr int kMeta = (kRing > kOut ? kRing : kOut);        // each warp: a group's key scales and minima
-  static constexpr int kStats = kMeta + kFewWarps * D * 4;           // each warp: (max, sum) of 16 rows, value exponent
-  static constexpr int kJoin = kStats + kFewWarps * (kFewRows * 8 + 16);
+  static constexpr int kStats = kMeta + WARPS * D * 4;           // each warp: (max, sum) of 16 rows, value exponent
+  static constexpr int kJoin = kStats + WARPS * (kFewRows * 8 + 16);
   static constexpr int kJoinStats = kJoin + kFewRows * D * 4;        // the CTA's own result, for its cluster
   static constexpr int kBars = kJoinStats + kFewRows * 8;
-  static constexpr int kBytes = kBars + kFewWarps * kFewStages * 8;
+  static constexpr int kBytes = kBars + WARPS * kFewStages * 8;
 };
 
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
@@ -377,12 +383,12 @@ struct FewWarp {
   }
 };
 
-template <int KIND, int D>
-__global__ void __launch_bounds__(kFewWarps * 32, 1) chunk_few_kernel(const __grid_constant__ ChunkAttnParams p, int splits) {
-  using L = FewSmem<KIND, D>;
+template <int KIND, int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_kernel(const __grid_constant__ ChunkAttnParams p, int splits) {
+  using L = FewSmem<KIND, D, WARPS>;
   using W = FewWarp<KIND, D>;
   using R = Rec<KIND, D>;
-  constexpr int kThreads = kFewWarps * 32;
+  constexpr int kThreads = WARPS * 32;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_addr(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) chunk_few_kernel(const __gr
   const int stored_groups = (job.stored + kGroup - 1) / kGroup, groups = stored_groups + (job.current ? 1 : 0);
   const int first = static_cast<int>(static_cast<int64_t>(groups) * rank / splits);
   const int last = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / splits);
-  const int mine = max(0, (last - first - warp + kFewWarps - 1) / kFewWarps);  // first + warp + 12 i
+  const int mine = max(0, (last - first - warp + WARPS - 1) / WARPS);  // first + warp + WARPS i
 
   // this warp's ring: group i of its own in stage i % stages
   const uint32_t ring = sbase + warp * kFewStages * L::kGroupBytes, bar = sbase + L::kBars + warp * kFewStages * 8;
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) chunk_few_kernel(const __gr
   // block ids of 32 of its groups at a time, one group a thread
   int2 ids = make_int2(0, 0);
   auto load_ids = [&](int i0) {
-    const int g = first + warp + (i0 + lane) * kFewWarps;
+    const int g = first + warp + (i0 + lane) * WARPS;
     if (i0 + lane < mine && g < stored_groups) {
       ids.x = table[2 * g];
       ids.y = 2 * g + 1 < (job.stored + kBlock - 1) / kBlock ? table[2 * g + 1] : -1;
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) chunk_few_kernel(const __gr
   auto issue = [&](int i) {  // whole warp
     if (i % 32 == 0) load_ids(i);
     const int x = __shfl_sync(0xffffffffu, ids.x, i % 32), y = __shfl_sync(0xffffffffu, ids.y, i % 32);
-    if (i < mine && first + warp + i * kFewWarps < stored_groups && lane == 0) {
+    if (i < mine && first + warp + i * WARPS < stored_groups && lane == 0) {
       const uint32_t s = i % kFewStages, dst = ring + s * L::kGroupBytes;
       mbar_arrive_expect_tx(bar + 8 * s, (y >= 0 ? 2 : 1) * R::kBytes);
       bulk_load(dst, p.arena + (static_cast<size_t>(x) * p.Hkv + job.hk) * R::kBytes, R::kBytes, bar + 8 * s, policy);
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) chunk_few_kernel(const __gr
   bool ok = true;
 #pragma unroll 1
   for (int i = 0; i < mine; ++i) {
-    const int g = first + warp + i * kFewWarps, t0 = g * kGroup, s = i % kFewStages;
+    const int g = first + warp + i * WARPS, t0 = g * kGroup, s = i % kFewStages;
     __syncwarp();      // the stage that comes next has been read by all
     issue(i + kFewStages - 1);
     float logit[4][4] = {};
@@ -502,9 +508,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) chunk_few_kernel(const __gr
   for (int i = threadIdx.x; i < rows * kQuads; i += kThreads) {
     const int row = i / kQuads, col = i % kQuads;
     float m = -INFINITY, sum = 0.f;
-    for (int k = 0; k < kFewWarps; ++k) m = fmaxf(m, stats[k * kFewRows + row].x);
+    for (int k = 0; k < WARPS; ++k) m = fmaxf(m, stats[k * kFewRows + row].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < kFewWarps; ++k) {
+    for (int k = 0; k < WARPS; ++k) {
       const float2 st = stats[k * kFewRows + row];
       if (st.x == -INFINITY) continue;  // it saw no key
       const float g = fast_exp2(st.x - m);

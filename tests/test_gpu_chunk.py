@@ -621,3 +621,21 @@ def test_outlier_channels_of_exact_keys(m, T):
     m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0]))
     out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([n]), k_cur=kc, v_cur=vc)
     check_rows(out, expect_rows("bf16", k, v, [n], q, [n], [T], 1.0, cur=(kc, vc)))
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2"])
+@pytest.mark.parametrize("B,H,d,n", [(1, 4, 128, 3000), (1, 16, 128, 2500), (10, 16, 64, 1200), (40, 16, 128, 300),
+                                     (13, 16, 128, 500), (64, 4, 64, 1500)])
+def test_few_rows_at_every_cta_size(m, kind, B, H, d, n):
+    """Grids from four pairs of sequence and head to some hundred: other CTA
+    sizes and splits of the context for each."""
+    lens = [n - 7 * (b % 5) for b in range(B)]
+    T = 3
+    kv, table, k, v = store(m, kind, B, H, d, n, H, lens)
+    q = seeded_bf16((B, T, H, d), 3, 0.3)
+    err = ints([0])
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([x - T for x in lens]), err_flag=err)
+    assert int(err) == 0
+    some = sorted({0, B // 2, B - 1})
+    check_rows(out[some], expect_rows(kind, k[some], v[some], [lens[b] for b in some], q[some],
+                                      [lens[b] - T for b in some], [T] * len(some), 1.0))
