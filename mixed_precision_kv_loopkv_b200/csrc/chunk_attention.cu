@@ -70,6 +70,31 @@ cudaError_t prepare_once(Kernel kern, size_t smem, int regs, int dev) {
   return cudaSuccess;
 }
 
+// Clusters of `splits` CTAs that the device holds at once (a cluster stays within
+// one group of SMs, so these are fewer than the SMs would give).
+template <int KIND, int D, int MT, typename Kernel>
+int64_t resident_clusters(Kernel kern, int splits, int threads, size_t smem, int dev) {
+  static std::mutex mu;
+  static int64_t cache[kMaxDevices][kMaxSplits + 1] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && cache[dev][splits]) return cache[dev][splits];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(splits, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = splits;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) clusters = 1;
+  if (dev >= 0) cache[dev][splits] = clusters;
+  return clusters;
+}
+
 template <int KIND, int D, int MT>
 cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
   using L = ChunkSmem<D, MT>;
@@ -87,47 +112,65 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
   const int64_t units = row_tiles * p.Hkv * p.chunk.B;
   const int64_t keys = static_cast<int64_t>(p.max_stored) + (p.k_cur.p ? p.chunk.T : 0);
   const int64_t key_tiles = (keys + kTileKeys - 1) / kTileKeys;
+  // as many splits as all run at once, of at least two tiles each
   int splits = 1;
-  while (splits < kMaxSplits && units * splits * 2 <= sm_count(dev) && key_tiles >= splits * 4) splits *= 2;
+  while (splits < kMaxSplits && key_tiles >= splits * 4 &&
+         units <= resident_clusters<KIND, D, MT>(kern, splits * 2, chunk_threads<MT>(), kSmem, dev))
+    splits *= 2;
   return launch_clusters(kern, units, splits, chunk_threads<MT>(), kSmem, stream, p, static_cast<int>(row_tiles));
 }
 
+// Few rows, CTAs of WARPS warps.  With `splits` 0 the best split is looked for:
+// its cost is compared with *best, and warps and splits are set if it is less.
 template <int KIND, int D, int WARPS>
-cudaError_t launch_few_w(const ChunkAttnParams& p, int64_t units, int splits, int dev, cudaStream_t stream) {
+cudaError_t few_w(const ChunkAttnParams& p, int64_t units, int64_t groups, int dev, int* warps, int* splits, int64_t* best,
+                  cudaStream_t stream) {
   using L = FewSmem<KIND, D, WARPS>;
   static_assert(kFewWarpsPerSm / WARPS * (L::kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
   static constexpr auto kern = chunk_few_kernel<KIND, D, WARPS>;
   const cudaError_t e = prepare_once<KIND, D, -WARPS>(kern, L::kBytes, 0, dev);
   if (e != cudaSuccess) return e;
-  return launch_clusters(kern, units, splits, WARPS * 32, L::kBytes, stream, p);
+  if (!best) return launch_clusters(kern, units, *splits, WARPS * 32, L::kBytes, stream, p);
+  auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const int64_t sms = sm_count(dev);
+  for (int s = 1; s <= kMaxSplits; s *= 2) {
+    const int64_t at_once = s == 1 ? sms * (kFewWarpsPerSm / WARPS)
+                                   : resident_clusters<KIND, D, -WARPS>(kern, s, WARPS * 32, L::kBytes, dev);
+    const int64_t waves = ceil_div(units, at_once);
+    // CTAs on the busiest SM; a cluster's fill an SM before they go to the next
+    int64_t load = ceil_div(units * s, sms);
+    const int64_t packed = s == 1 ? 1 : s < kFewWarpsPerSm / WARPS ? s : kFewWarpsPerSm / WARPS;
+    load = load > waves * packed ? load : waves * packed;
+    const int64_t busiest = load * ceil_div(groups, s), serial = waves * ceil_div(groups, s * WARPS) * 6;
+    const int64_t cost = (busiest > serial ? busiest : serial) + waves * (s == 1 ? 25 : 45);
+    if (cost < *best) *best = cost, *splits = s, *warps = WARPS;
+  }
+  return cudaSuccess;
 }
 
 // Few rows: the CTA size and split of least estimated time, in the time that an
 // SM with twelve warps at work takes a 32-token group (440 cycles): what the
 // busiest SM has to read, or six for each group that a warp takes one after
-// another; and for each wave of CTAs their start and end, 25, or 55 as clusters.
+// another; and for each wave of CTAs their start and end, 25, or 45 as clusters.
 // Measured, 512 (sequence, head) pairs of 4100 tokens: CTAs of 12 warps 144 us,
 // of 6 warps 130, of 3 warps 122 (one wave), of 3 warps in clusters of two 131.
-// With 16 pairs of 16384 tokens, 12 warps in clusters of eight put every SM to work.
+// 16 pairs of 16384 tokens: 12 warps alone 118 us, in clusters of four 38, of
+// eight (which do not all run at once) 50; 16 pairs of 1024: alone 16, four 12.
 template <int KIND, int D>
 cudaError_t launch_few(const ChunkAttnParams& p, cudaStream_t stream) {
   const int dev = current_device();
-  const int64_t units = static_cast<int64_t>(p.Hkv) * p.chunk.B, sms = sm_count(dev);
+  const int64_t units = static_cast<int64_t>(p.Hkv) * p.chunk.B;
   const int64_t groups = (static_cast<int64_t>(p.max_stored) + kGroup - 1) / kGroup + (p.k_cur.p ? 1 : 0);
-  auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  int splits = 1, warps = kFewWarpsPerSm;
+  int warps = kFewWarpsPerSm, splits = 1;
   int64_t best = INT64_MAX;
-  for (int w = kFewWarpsPerSm; w >= 3; w /= 2)
-    for (int s = 1; s <= kMaxSplits; s *= 2) {
-      const int64_t waves = ceil_div(units * s, sms * (kFewWarpsPerSm / w));
-      const int64_t busiest = ceil_div(units * s, sms) * ceil_div(groups, s), serial = waves * ceil_div(groups, s * w) * 6;
-      const int64_t cost = (busiest > serial ? busiest : serial) + waves * (s == 1 ? 25 : 55);
-      if (cost < best) best = cost, splits = s, warps = w;
-    }
+  cudaError_t e = few_w<KIND, D, 12>(p, units, groups, dev, &warps, &splits, &best, stream);
+  if (e == cudaSuccess) e = few_w<KIND, D, 6>(p, units, groups, dev, &warps, &splits, &best, stream);
+  if (e == cudaSuccess) e = few_w<KIND, D, 3>(p, units, groups, dev, &warps, &splits, &best, stream);
+  if (e != cudaSuccess) return e;
   switch (warps) {
-    case 3: return launch_few_w<KIND, D, 3>(p, units, splits, dev, stream);
-    case 6: return launch_few_w<KIND, D, 6>(p, units, splits, dev, stream);
-    default: return launch_few_w<KIND, D, 12>(p, units, splits, dev, stream);
+    case 3: return few_w<KIND, D, 3>(p, units, groups, dev, &warps, &splits, nullptr, stream);
+    case 6: return few_w<KIND, D, 6>(p, units, groups, dev, &warps, &splits, nullptr, stream);
+    default: return few_w<KIND, D, 12>(p, units, groups, dev, &warps, &splits, nullptr, stream);
   }
 }
 
