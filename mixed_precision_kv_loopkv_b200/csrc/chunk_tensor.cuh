@@ -60,8 +60,7 @@ struct ChunkSmem {
   static constexpr int kBars = kStats + MT * 128 * 8;
   static constexpr int kBarCount = 9 + 2 * 6;
   static constexpr int kTmem = kBars + kBarCount * 8;
-  static constexpr int kFlags = kTmem + 4;
-  static constexpr int kBytes = kFlags + 4;
+  static constexpr int kBytes = kTmem + 8;
   static constexpr int kPartial = kK;                // fp32 partial O over the stages: MT 128 D 4 = MT kTile 2 <= 4 kTile
 };
 
@@ -579,7 +578,6 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
   auto s_free = [&](int m) { return bars + 88 + 8 * m; };                       // and have been read
   auto p_full = [&](int m, int buf) { return bars + 104 + 16 * m + 8 * buf; };  // its weights are there
   auto o_done = [&](int m, int buf) { return bars + 136 + 16 * m + 8 * buf; };  // and are in O
-  volatile int* gave_up = reinterpret_cast<volatile int*>(smem + L::kFlags);
   float* k_exp = reinterpret_cast<float*>(smem + L::kKExp);
   int* v_exp = reinterpret_cast<int*>(smem + L::kVExp);
 
@@ -600,7 +598,6 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       }
     }
     fence_mbar_init();
-    *gave_up = 0;
   }
   if (warp == kIssueWarp) tmem_alloc<kTmemCols>(sbase + L::kTmem);
   tc_fence_before();
