@@ -150,11 +150,20 @@ def _ints(t, what, shape, dev):
     return t.data_ptr()
 
 
-def _output(out, what, shape, dev, inputs=(), itself=None):
+def _new(shape, dev, stream, fill=True):
+    """A new output, made (and filled with zeros) on the stream of the call."""
+    make = torch.zeros if fill else torch.empty
+    if stream is None:
+        return make(shape, dtype=torch.bfloat16, device=f"cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=torch.bfloat16, device=f"cuda:{dev}")
+
+
+def _output(out, what, shape, dev, stream, inputs=(), itself=None):
     """The contiguous output, zeros if not given.  It must lie apart from every
     input (name, tensor, its rows) but ``itself``, which it may be (in place)."""
     if out is None:
-        return torch.zeros(shape, dtype=torch.bfloat16, device=f"cuda:{dev}")
+        return _new(shape, dev, stream)
     if not _is(out, torch.bfloat16, shape, dev):
         _refuse(out, what, torch.bfloat16, shape, dev)
     ptr = out.data_ptr()
@@ -231,8 +240,8 @@ def loopkv_norm_rope(rotary: Rotary, q, k, start_pos, new_lens=None, q_out=None,
         kv_heads = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
         kr = _rows(k, "k", (batch, tokens, kv_heads, dim), dev)
         ins.append(("k", k, kr))
-    q_out = _output(q_out, "q_out", q.shape, dev, ins, "q") if q is not None else None
-    k_out = _output(k_out, "k_out", k.shape, dev, ins, "k") if k is not None else None
+    q_out = _output(q_out, "q_out", q.shape, dev, stream, ins, "q") if q is not None else None
+    k_out = _output(k_out, "k_out", k.shape, dev, stream, ins, "k") if k is not None else None
     if q is not None and k is not None and not _apart(q_out, k_out):
         raise ValueError("q_out overlaps k_out")
     lens = None if new_lens is None else _ints(new_lens, "new_lens", (batch,), dev)
@@ -262,7 +271,7 @@ def loopkv_rope_append(kv: KVCells, loop: int, layer: int, rotary, q, k_new, v_n
     if q is not None:
         shape = (batch, tokens, kv.num_heads, kv.head_dim)
         qr = _rows(q, "q", shape, dev)
-        q_out = _output(q_out, "q_out", shape, dev, (("q", q, qr), ("k_new", k_new, kr), ("v_new", v_new, vr)), "q")
+        q_out = _output(q_out, "q_out", shape, dev, stream, (("q", q, qr), ("k_new", k_new, kr), ("v_new", v_new, vr)), "q")
     else:
         q_out = None
     lens = None if new_lens is None else _ints(new_lens, "new_lens", (batch,), dev)
@@ -285,7 +294,7 @@ def loopkv_read_tokens(kv: KVCells, loop: int, layer: int, block_table, seq_lens
         raise ValueError("start_pos must be [batch], num_tokens not negative")
     batch = start_pos.shape[0]
     shape = (batch, num_tokens, kv.num_kv_heads, kv.head_dim)
-    k_out, v_out = _output(k_out, "k_out", shape, dev), _output(v_out, "v_out", shape, dev)
+    k_out, v_out = _output(k_out, "k_out", shape, dev, stream), _output(v_out, "v_out", shape, dev, stream)
     if not _apart(k_out, v_out):
         raise ValueError("k_out overlaps v_out")
     _call(_lib.loopkv_read_tokens, "loopkv_read_tokens", dev, stream, kv.cfg, kv.cells, loop, layer,
@@ -318,9 +327,9 @@ def loopkv_chunk_attention(kv: KVCells, loop: int, layer: int, q, block_table, s
         kr, vr = _rows(k_cur, "k_cur", rows, dev), _rows(v_cur, "v_cur", rows, dev)
         ins += [("k_cur", k_cur, kr), ("v_cur", v_cur, vr)]
     if out is None and new_lens is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=f"cuda:{dev}")  # every row is written
+        out = _new(shape, dev, stream, fill=False)  # every row is written
     else:
-        out = _output(out, "out", shape, dev, ins)
+        out = _output(out, "out", shape, dev, stream, ins)
     lens = None if new_lens is None else _ints(new_lens, "new_lens", (batch,), dev)
     _call(_lib.loopkv_chunk_attention, "loopkv_chunk_attention", dev, stream, kv.cfg, kv.cells, loop, layer, qr[0],
           kr and kr[0], vr and vr[0], _ints(block_table, "block_table", (batch, kv.max_blocks_per_seq), dev),

@@ -151,9 +151,10 @@ class LoopedChunkStep:
             raise ValueError("one rotary for all layers or one for each")
         self.sm_scale, self.max_seq_len, self.err_flag = sm_scale, max_seq_len, err_flag
         self.cells = list(range(len(kv.plan_codes))) if cells is None else sorted(cells)
-        # rotated queries (and a reuse cell's keys): one cell's at a time
+        # rotated queries (and a reuse cell's keys): one cell's at a time; what a
+        # chunk does not write there it does not read
         shapes = {"q": self.q[self.cells[0]].shape, "k": self.k[self.cells[0]].shape} if self.cells else {}
-        self._rows = {name: torch.zeros(shape, dtype=torch.bfloat16, device=start.device) for name, shape in shapes.items()}
+        self._rows = {name: torch.empty(shape, dtype=torch.bfloat16, device=start.device) for name, shape in shapes.items()}
 
     def launches_per_step(self) -> int:
         return 2 * len(self.cells)

@@ -639,3 +639,24 @@ def test_few_rows_at_every_cta_size(m, kind, B, H, d, n):
     some = sorted({0, B // 2, B - 1})
     check_rows(out[some], expect_rows(kind, k[some], v[some], [lens[b] for b in some], q[some],
                                       [lens[b] - T for b in some], [T] * len(some), 1.0))
+
+
+def test_new_outputs_belong_to_the_stream_of_the_call(m):
+    """A new output is filled on the stream that the call goes to: work that the
+    current stream still has before it does not come after the result."""
+    B, H, d = 2, 2, 64
+    kv, table, k, v = store(m, "q4", B, H, d, 64, H, [40, 33])
+    q, s, lens, r = seeded_bf16((B, 4, H, d), 3), ints([36, 29]), ints([4, 3]), m.Rotary()
+    stored, skip = ints([40, 33]), ints([-1, -1])
+    calls = [lambda **kw: m.loopkv_chunk_attention(kv, 0, 0, q, table, s, lens, **kw),
+             lambda **kw: m.loopkv_norm_rope(r, q, None, s, lens, **kw)[0],
+             lambda **kw: m.loopkv_read_tokens(kv, 0, 0, table, stored, s, 4, **kw)[1],
+             lambda **kw: m.loopkv_rope_append(kv, 0, 0, r, q, k[:, :4], v[:, :4], table, skip, **kw)]
+    want = [c() for c in calls]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        torch.cuda._sleep(20_000_000)
+        got = c(stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, w)
