@@ -13,6 +13,9 @@ import torch
 from .loopkv import KVCells, LoopKVError, library, loopkv_cells, loopkv_config
 
 
+_BF16, _INT32 = torch.bfloat16, torch.int32
+
+
 class loopkv_rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
@@ -119,32 +122,32 @@ def _refuse(t, what, dtype, shape, dev):
 
 
 def _is(t, dtype, shape, dev):
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+    try:
+        return t.dtype is dtype and t.get_device() == dev and t.shape == shape
+    except AttributeError:  # no tensor
+        return False
 
 
 def _rows(t, what, shape, dev):
     """Rows bf16 [batch, tokens, heads, D], last dimension contiguous, others
     strided: the C struct, and the first and one past the last byte they reach."""
-    if not _is(t, torch.bfloat16, shape, dev):
-        _refuse(t, what, torch.bfloat16, shape, dev)
+    if not _is(t, _BF16, shape, dev):
+        _refuse(t, what, _BF16, shape, dev)
     b, n, h, d = shape
     sb, st, sh, sd = t.stride()
-    if b == 1:
-        sb = 0
-    if n == 1:
-        st = 0
-    if h == 1:
-        sh = 0
     ptr = t.data_ptr()
-    if ((sb | st | sh) & 7 or ptr & 15 or sd != 1) and t.numel():
-        raise ValueError(f"{what} must be contiguous in its last dimension, 16-byte aligned, with strides that are "
-                         "multiples of 8 elements")
+    if (sb | st | sh) & 7 or ptr & 15 or sd != 1:
+        # the stride of a dimension of one says nothing
+        sb, st, sh = (0 if k == 1 else x for k, x in zip(shape, (sb, st, sh)))
+        if ((sb | st | sh) & 7 or ptr & 15 or sd != 1) and t.numel():
+            raise ValueError(f"{what} must be contiguous in its last dimension, 16-byte aligned, with strides that are "
+                             "multiples of 8 elements")
     return loopkv_rows(ptr, sb, st, sh), ptr, ptr + 2 * ((b - 1) * sb + (n - 1) * st + (h - 1) * sh + d)
 
 
 def _ints(t, what, shape, dev):
-    if not _is(t, torch.int32, shape, dev):
-        _refuse(t, what, torch.int32, shape, dev)
+    if not _is(t, _INT32, shape, dev):
+        _refuse(t, what, _INT32, shape, dev)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
@@ -164,14 +167,14 @@ def _output(out, what, shape, dev, stream, inputs=(), itself=None):
     input (name, tensor, its rows) but ``itself``, which it may be (in place)."""
     if out is None:
         return _new(shape, dev, stream)
-    if not _is(out, torch.bfloat16, shape, dev):
-        _refuse(out, what, torch.bfloat16, shape, dev)
+    if not _is(out, _BF16, shape, dev):
+        _refuse(out, what, _BF16, shape, dev)
     ptr = out.data_ptr()
     if not out.is_contiguous() or ptr & 15:
         raise ValueError(f"{what} must be contiguous and 16-byte aligned")
     end = ptr + 2 * out.numel()
     for name, x, rows in inputs:
-        if x is not None and rows[1] < end and ptr < rows[2]:
+        if rows[1] < end and ptr < rows[2]:
             if not (name == itself and rows[1] == ptr and x.is_contiguous()):
                 raise ValueError(f"{what} overlaps {name}")
     return out
@@ -198,7 +201,10 @@ def _cell_device(kv: KVCells, loop: int, layer: int):
     arena = kv.arenas[kv.source_cell(loop * kv.num_layers + layer)]
     if arena is None:
         raise ValueError(f"cell ({loop}, {layer}) has no storage")
-    return _device_of(arena, "the cell's storage")
+    dev = arena.get_device()
+    if dev < 0:
+        raise ValueError("the cell's storage must be on a CUDA device")
+    return dev
 
 
 def _call(fn, name, dev, stream, *args):
@@ -206,7 +212,7 @@ def _call(fn, name, dev, stream, *args):
     unless another of its streams is given."""
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    elif stream.device.index != dev:
+    elif stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     if torch.cuda.current_device() == dev:
         st = fn(*args, stream.cuda_stream)

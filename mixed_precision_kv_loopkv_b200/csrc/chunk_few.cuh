@@ -250,7 +250,7 @@ struct FewWarp {
       }
       v_ref = v_new;
     }
-    const int de = max(ve - v_ref, -100);           // at most 4
+    const int de = max(ve - v_ref, kLeastShift);    // at most 4
     const float back = __int_as_float((127 - de) << 23);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -42,10 +42,16 @@ constexpr int kExpRing = 4;
 constexpr int kPolyPair = 3;                         // of four pairs of weights, the one worked out on the FMA units
 
 // A block's keys (values) are stored as x 2^-e with e such that the largest is
-// in [2^-7, 2^-6): then 2^24 times a 4-bit scale, at most 2^24 (2 2^-6 / 15)
-// (1 + 2^-8) < 35200, is a finite fp16 number, and the code itself, read as a
-// subnormal fp16 number (code 2^-24), needs no conversion.
+// in [2^-7, 2^-6): then 2^24 times a 4-bit scale, at most 2^24 2 2^-6 / 15 <
+// 35000 (2^22 times a 2-bit one: 2^22 2 2^-6 / 3 < 43700), is a finite fp16
+// number, and the code itself, read as a subnormal fp16 number (code 2^-24; 2-bit
+// codes stand two bits higher), needs no conversion.
 constexpr int kTopExp = -6;
+
+// A value block's exponent below that of the outputs counts down to 2^-60: its
+// share is nothing then, and its weights stay far above the 2^-126 that the
+// exponentials end at.
+constexpr int kLeastShift = -60;
 
 template <int D, int MT>
 struct ChunkSmem {
@@ -833,7 +839,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       const float base = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int de = max(vexp[c] - v_ref, -100);  // at most 4
+        const int de = max(vexp[c] - v_ref, kLeastShift);  // at most 4
         const float off = static_cast<float>(de) - base;
         const uint64_t f2 = pack2(f[c], f[c]), off2 = pack2(off, off);
         uint64_t part = 0;  // two sums of zero

@@ -660,3 +660,21 @@ def test_new_outputs_belong_to_the_stream_of_the_call(m):
         got = c(stream=side)
         torch.cuda.synchronize()
         assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("kind", ["q4", "bf16"])
+@pytest.mark.parametrize("T", [4, 130])
+def test_zero_values_and_values_of_far_apart_sizes(m, kind, T):
+    """Most blocks' values are exactly zero, or 2^-40 of the others: they still
+    take their weights out of the rest."""
+    B, H, d, n = 1, 2, 128, 1600
+    kv, table = cell_for(m, kind, B, H, d, n)
+    k, v = seeded_bf16((B, n, H, d), 1), seeded_bf16((B, n, H, d), 2)
+    v[:, 64:1200] = 0
+    v[:, 1200:1500] *= 2.0**-40
+    m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0]))
+    q = seeded_bf16((B, T, H, d), 3, 1.0)
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([n - T]))
+    step = max(1, T // 5)
+    check_rows(out[:, ::step], [(b, h, w[::step], e[::step]) for b, h, w, e in
+                                expect_rows(kind, k, v, [n], q, [n - T], [T], 1.0)])
