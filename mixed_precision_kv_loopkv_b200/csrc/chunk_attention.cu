@@ -120,8 +120,8 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
   return launch_clusters(kern, units, splits, chunk_threads<MT>(), kSmem, stream, p, static_cast<int>(row_tiles));
 }
 
-// Few rows, CTAs of WARPS warps.  With `splits` 0 the best split is looked for:
-// its cost is compared with *best, and warps and splits are set if it is less.
+// Few rows, CTAs of WARPS warps.  With `best`, each split's cost is compared with
+// it, and it, warps and splits are set where that is less; without, the launch.
 template <int KIND, int D, int WARPS>
 cudaError_t few_w(const ChunkAttnParams& p, int64_t units, int64_t groups, int dev, int* warps, int* splits, int64_t* best,
                   cudaStream_t stream) {
