@@ -678,3 +678,24 @@ def test_zero_values_and_values_of_far_apart_sizes(m, kind, T):
     step = max(1, T // 5)
     check_rows(out[:, ::step], [(b, h, w[::step], e[::step]) for b, h, w, e in
                                 expect_rows(kind, k, v, [n], q, [n - T], [T], 1.0)])
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("d,interleaved", [(64, False), (128, True)])
+def test_norm_of_one_side_only(m, which, d, interleaved):
+    """A weight for queries or for keys alone, heads of both in one thread's item."""
+    table = CO.rope_angles(40, d)
+    w = seeded_bf16((d,), 7, 0.2) + 1
+    r = m.Rotary(torch.from_numpy(table).cuda(), interleaved=interleaved, eps=1e-5, **{which + "_weight": w})
+    q, k, v = fused_rows(2, 9, 3, 3, d, seed=5)
+    start = ints([0, 20])
+    q_out, k_out = m.loopkv_norm_rope(r, q, k, start)
+    for x, o, name in ((q, q_out, "q"), (k, k_out, "k")):
+        for b, s in enumerate([0, 20]):
+            want = CO.norm_rope(host(x[b]), s + np.arange(9), table, interleaved, host(w) if name == which else None, 1e-5)
+            assert np.array_equal(host(o[b]), want)
+    kv, bt = cell_for(m, "bf16", 2, 3, d, 40)
+    got = m.loopkv_rope_append(kv, 0, 0, r, q, k, v, bt, start)
+    assert torch.equal(got, q_out)
+    kk, vv = m.loopkv_read_tokens(kv, 0, 0, bt, ints([9, 29]), start, 9)
+    assert torch.equal(kk, k_out) and torch.equal(vv, v.contiguous())
