@@ -15,6 +15,12 @@ from .loopkv import KVCells, LoopKVError, library, loopkv_cells, loopkv_config
 
 _BF16, _INT32 = torch.bfloat16, torch.int32
 
+try:  # the handle alone: a Stream object takes a microsecond to make
+    from torch._C import _cuda_getCurrentRawStream as _current_stream
+except ImportError:
+    def _current_stream(dev):
+        return torch.cuda.current_stream(dev).cuda_stream
+
 
 class loopkv_rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
@@ -211,14 +217,16 @@ def _call(fn, name, dev, stream, *args):
     """Call on the tensors' device, whichever is current, on its current stream
     unless another of its streams is given."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        handle = _current_stream(dev)
     elif stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        st = fn(*args, stream.cuda_stream)
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st:
         raise LoopKVError(st, name)
 
@@ -246,9 +254,9 @@ def loopkv_norm_rope(rotary: Rotary, q, k, start_pos, new_lens=None, q_out=None,
         kv_heads = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
         kr = _rows(k, "k", (batch, tokens, kv_heads, dim), dev)
         ins.append(("k", k, kr))
-    q_out = _output(q_out, "q_out", q.shape, dev, stream, ins, "q") if q is not None else None
-    k_out = _output(k_out, "k_out", k.shape, dev, stream, ins, "k") if k is not None else None
-    if q is not None and k is not None and not _apart(q_out, k_out):
+    q_out = _output(q_out, "q_out", q.shape, dev, stream, ins, "q") if qr else None
+    k_out = _output(k_out, "k_out", k.shape, dev, stream, ins, "k") if kr else None
+    if qr and kr and not _apart(q_out, k_out):
         raise ValueError("q_out overlaps k_out")
     lens = None if new_lens is None else _ints(new_lens, "new_lens", (batch,), dev)
     _call(_lib.loopkv_norm_rope, "loopkv_norm_rope", dev, stream, rotary.struct, dim, heads, kv_heads,
