@@ -61,7 +61,8 @@ __device__ __forceinline__ void load_turn(const RotaryView& r, int pos, int sub,
 // x^2 of a bf16 pair added to a 64-bit sum.  A bf16 number's exponent and
 // mantissa are moved into a double's, which costs two integer operations where
 // the conversion instruction runs at an eighth of their rate; 0 comes out as
-// 2^-127, whose square is nothing beside eps (at least 1e-30).
+// 2^-127, whose square is nothing beside eps (at least 1e-30), and infinities and
+// NaN as 2^128 and more: a sum of 2^256, for which see any_huge.
 __device__ __forceinline__ double add_squares(uint32_t w, double sum) {
   const double a = __hiloint2double(static_cast<int>((w & 0x7FFFu) * 8192u + 0x38000000u), 0);
   const double b = __hiloint2double(static_cast<int>(((w & 0x7FFF0000u) >> 3) + 0x38000000u), 0);
@@ -72,11 +73,32 @@ __device__ __forceinline__ double squares(const uint4& raw) {
   return add_squares(raw.w, add_squares(raw.z, add_squares(raw.y, add_squares(raw.x, 0.0))));
 }
 
-// fp32(1 / sqrt(mean of a row's squares + eps)), sum the thread's part.
-template <int D>
-__device__ __forceinline__ float inverse_norm(double sum, double eps) {
+// The same with every number converted: infinite or NaN where an entry is.
+__device__ __noinline__ double exact_squares(uint4 raw) {
+  float x[8];
+  unpack8(raw, x);
+  double sum = 0.0;
 #pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
+  return sum;
+}
+
+// Whether one of the warp's rows may hold an infinity or a NaN (or its finite
+// squares add up to 2^255 and more): its sum is to be taken of exact_squares.
+__device__ __forceinline__ bool any_huge(double sum) {
+  return __any_sync(0xffffffffu, __double2hiint(sum) >= (1023 + 255) << 20);
+}
+
+// fp32(1 / sqrt(mean of a row's squares + eps)), raw the thread's part.
+template <int D>
+__device__ __forceinline__ float inverse_norm(const uint4& raw, double eps) {
+  auto row_sum = [](double sum) {
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  };
+  double sum = row_sum(squares(raw));
+  if (any_huge(sum)) sum = row_sum(exact_squares(raw));
   return static_cast<float>(rsqrt(sum * (1.0 / D) + eps));
 }
 
@@ -85,13 +107,17 @@ __device__ __forceinline__ float inverse_norm(double sum, double eps) {
 // one root instead of four.
 template <int D>
 __device__ __forceinline__ float inverse_norm4(const uint4 (&raw)[4], double eps, int sub) {
-  const double q[4] = {squares(raw[0]), squares(raw[1]), squares(raw[2]), squares(raw[3])};
   const bool odd = sub & 1, high = sub & 2;
-  const double a = (odd ? q[1] : q[0]) + __shfl_xor_sync(0xffffffffu, odd ? q[0] : q[1], 1);
-  const double b = (odd ? q[3] : q[2]) + __shfl_xor_sync(0xffffffffu, odd ? q[2] : q[3], 1);
-  double sum = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
+  auto row_sum = [&](double q0, double q1, double q2, double q3) {
+    const double a = (odd ? q1 : q0) + __shfl_xor_sync(0xffffffffu, odd ? q0 : q1, 1);
+    const double b = (odd ? q3 : q2) + __shfl_xor_sync(0xffffffffu, odd ? q2 : q3, 1);
+    double sum = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
 #pragma unroll
-  for (int o = D / 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = D / 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  };
+  double sum = row_sum(squares(raw[0]), squares(raw[1]), squares(raw[2]), squares(raw[3]));
+  if (any_huge(sum)) sum = row_sum(exact_squares(raw[0]), exact_squares(raw[1]), exact_squares(raw[2]), exact_squares(raw[3]));
   return static_cast<float>(rsqrt(sum * (1.0 / D) + eps));
 }
 
@@ -308,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppe
         load_turn<PAIRS>(rot, pos, sub, turn);
       }
       float x[8];
-      const float inv_norm = w ? inverse_norm<D>(squares(k_raw), rot.eps) : 1.f;
+      const float inv_norm = w ? inverse_norm<D>(k_raw, rot.eps) : 1.f;
       weigh_rotate<D, PAIRS>(rot, w, inv_norm, turn, sub, k_raw, x);
       uint8_t* rec = here ? record_at<KIND, D>(cell, pos) : nullptr;
       if (!rec) continue;
@@ -349,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppe
         load_turn<PAIRS>(rot, pos, sub, turn);
       }
       float x[8];
-      const float inv_norm = w ? inverse_norm<D>(squares(k_raw), rot.eps) : 1.f;
+      const float inv_norm = w ? inverse_norm<D>(k_raw, rot.eps) : 1.f;
       weigh_rotate<D, PAIRS>(rot, w, inv_norm, turn, sub, k_raw, x);
       // the value row: groups of 32 channels are four neighbouring threads
       float v[8];
@@ -504,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppe
           raw = *reinterpret_cast<const uint4*>(row_at(p.k, b, pos - start, h) + 8 * sub);
         }
         float x[8];
-        const float inv_norm = w ? inverse_norm<D>(squares(raw), rot.eps) : 1.f;
+        const float inv_norm = w ? inverse_norm<D>(raw, rot.eps) : 1.f;
         weigh_rotate<D, PAIRS>(rot, w, inv_norm, turn, sub, raw, x);
         if (here) *reinterpret_cast<uint4*>(res + r * D + 8 * sub) = pack8(x);
       }
