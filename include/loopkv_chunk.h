@@ -91,7 +91,8 @@ LOOPKV_API loopkv_status loopkv_norm_rope(const loopkv_rotary* rotary, int32_t h
  * by loopkv_quantize_append of them and the values would have stored, for
  * ragged chunks in one launch.  The queries (optional) are normed, rotated and
  * written to q_out in the same launch.
- *   rotary       : NULL stores the keys as they are (q must then be NULL)
+ *   rotary       : NULL stores the keys as they are, any NaN as 0x7FFF (q must
+ *                  then be NULL)
  *   q            : optional rows of num_heads heads, q_out as for loopkv_norm_rope
  *   k_new, v_new : rows of num_kv_heads heads
  * Errors: as loopkv_quantize_append and loopkv_norm_rope.

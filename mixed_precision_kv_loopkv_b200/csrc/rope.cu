@@ -238,7 +238,7 @@ __device__ __forceinline__ bool ordinary(float s) { return s > 0x1p-100f && s < 
 // rint of four rounded quotients a / s, given their estimates t within 3e-6,
 // where one of them lies within 1e-5 of a half h.  By the sign of the exact
 // remainder a - h s; where that is neither zero nor 2^-18 s away from it, or
-// the scale out of the ordinary, by the quotient itself.
+// the scale out of the ordinary, by the quotient itself.  0 for a NaN.
 template <int BITS>
 __device__ __noinline__ float4 settle_codes(float4 a, float4 s, float4 t) {
   constexpr float kTop = static_cast<float>((1 << BITS) - 1);
@@ -249,6 +249,8 @@ __device__ __noinline__ float4 settle_codes(float4 a, float4 s, float4 t) {
     r[i] = rintf(tt[i]);
     if (!ordinary(ss[i])) {
       r[i] = ss[i] == 0.f ? 0.f : fminf(fmaxf(rintf(exact_quotient(aa[i], ss[i])), 0.f), kTop);
+    } else if (aa[i] != aa[i]) {
+      r[i] = 0.f;
     } else if (fabsf(tt[i] - r[i]) > 0.49999f) {
       const float h = r[i] > tt[i] ? r[i] - 0.5f : r[i] + 0.5f, rem = fmaf(-h, ss[i], aa[i]);
       r[i] = rem == 0.f ? rintf(h) : rem > 0.f ? h + 0.5f : h - 0.5f;
@@ -263,7 +265,8 @@ __device__ __noinline__ float4 settle_codes(float4 a, float4 s, float4 t) {
 // bits.  t = (x - mn) * (1 / s) is within 3e-6 of the rounded quotient, so where
 // it is more than 1e-5 away from a half both round to the same integer (half to
 // even by adding 1.5 2^23 and taking it off again).  bf16 numbers meet halves
-// often enough (one in some thousand) for those to have a way of their own.
+// often enough (one in some thousand) for those to have a way of their own, and
+// a NaN, which the minimum and the maximum here keep, takes that too.
 // The four are put together as floats, exactly.
 template <int BITS>
 __device__ __forceinline__ uint32_t quick_codes(const float* x, const float (&s)[4], const float (&mn)[4],
@@ -272,11 +275,11 @@ __device__ __forceinline__ uint32_t quick_codes(const float* x, const float (&s)
   float r[4], t[4], off = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    t[i] = fminf(__fmul_rn(__fsub_rn(x[i], mn[i]), inv[i]), kTop);
+    t[i] = min_nan(__fmul_rn(__fsub_rn(x[i], mn[i]), inv[i]), kTop);
     r[i] = __fsub_rn(__fadd_rn(t[i], kRound), kRound);
-    off = fmaxf(off, fabsf(__fsub_rn(t[i], r[i])));
+    off = max_nan(off, fabsf(__fsub_rn(t[i], r[i])));
   }
-  if (off > 0.49999f || odd) {
+  if (!(off <= 0.49999f) || odd) {
     const float4 q = settle_codes<BITS>(
         make_float4(__fsub_rn(x[0], mn[0]), __fsub_rn(x[1], mn[1]), __fsub_rn(x[2], mn[2]), __fsub_rn(x[3], mn[3])),
         make_float4(s[0], s[1], s[2], s[3]), make_float4(t[0], t[1], t[2], t[3]));
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppe
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       }
       if (here) {
-        const uint4 packed = pack8(x);
+        uint4 packed = pack8(x);
         *reinterpret_cast<uint4*>(tile + r * kStride + 16 * sub) = packed;
         if (!complete && (gi == 0 || !begun)) *reinterpret_cast<uint4*>(res + r * D + 8 * sub) = packed;
         const float s_b = quick_scale<BITS>(mn, mx), inv = __frcp_rn(s_b);

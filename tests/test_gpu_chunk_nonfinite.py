@@ -56,3 +56,47 @@ def test_norms_of_rows_that_are_not_finite(m, d, rot, interleaved, heads, kv_hea
                 want = CO.norm_rope(host(x[b]), start[b] + np.arange(T), **a)
                 for o in outs:
                     assert np.array_equal(host(o[b]), want, equal_nan=True)
+
+
+def same_bytes(a, b, lens):
+    assert torch.equal(a.arenas[0], b.arenas[0])
+    if a.residuals[0] is not None:
+        for i, n in enumerate(lens):
+            assert torch.equal(bits(a.residuals[0][i, :, : n % 32]), bits(b.residuals[0][i, :, : n % 32]))
+
+
+def odd_entries(x, seed):
+    """Single entries, whole 32-channel groups and whole 32-token columns of x [B, T, heads, D] that are not finite."""
+    g = torch.Generator().manual_seed(seed)
+    B, T, H, D = x.shape
+    for value in (NAN, INF, -INF, NAN, INF, 3.3e38, -3.3e38):
+        for _ in range(6):
+            b, t, h, c = (int(torch.randint(0, n, (1,), generator=g)) for n in x.shape)
+            x[b, t, h, c] = value
+        x[b, (t + 5) % T, h, c // 32 * 32: c // 32 * 32 + 32] = value
+        x[b, : T // 32 * 32, h, (c + 1) % D] = value
+    bits(x)[0, 1, 0, 3], bits(x)[0, 2, 0, 4] = -1, 0x7F81        # NaN of other bits
+    return x
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("turned", [False, True])
+def test_append_of_what_is_not_finite(m, kind, d, turned):
+    """The bytes of norm_rope and quantize_append, NaN and infinities included."""
+    B, hkv, steps = 3, 2, [[70, 64, 5], [1, 31, 27], [33, 1, 64]]
+    r = rotary_for(m, d, d // 2, False, True)[0] if turned else None
+    got, table = cell_for(m, kind, B, hkv, d, 200)
+    want, _ = cell_for(m, kind, B, hkv, d, 200)
+    have = [0] * B
+    for step, lens in enumerate(steps):
+        T = max(lens)
+        k, v = (odd_entries(seeded_bf16((B, T, hkv, d), 40 + 2 * step + i), 7 + 2 * step + i) for i in range(2))
+        start = ints(have)
+        m.loopkv_rope_append(got, 0, 0, r, None, k, v, table, start, ints(lens))
+        k_in = m.loopkv_norm_rope(r or m.Rotary(), None, k, start, ints(lens))[1]
+        for b, n in enumerate(lens):
+            one = ints([have[b] if i == b else -1 for i in range(B)])
+            m.loopkv_quantize_append(want, 0, 0, k_in[:, :n].contiguous(), v[:, :n].contiguous(), table, one)
+        have = [a + n for a, n in zip(have, lens)]
+        same_bytes(got, want, have)
