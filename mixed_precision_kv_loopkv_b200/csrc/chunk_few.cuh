@@ -230,11 +230,12 @@ struct FewWarp {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       f[i] = fmaxf(row_scale[i] * k, FLT_MIN);  // not zero, for -inf's sake
-      float t = fmaxf(max3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), max3(s[1][2 * i + 1], s[2][2 * i], s[2][2 * i + 1]));
-      t = max3(t, s[3][2 * i], s[3][2 * i + 1]) * f[i];
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      top[i] = t > m_ref[i] + 8.f ? t : m_ref[i];   // follow only what is 2^8 above
+      float t = max_nan(max3_nan(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), max3_nan(s[1][2 * i + 1], s[2][2 * i], s[2][2 * i + 1]));
+      t = max3_nan(t, s[3][2 * i], s[3][2 * i + 1]) * f[i];
+      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      t = t < INFINITY ? t : NAN;                   // +inf: its weight is inf - inf
+      top[i] = t <= m_ref[i] + 8.f ? m_ref[i] : t;  // follow only what is 2^8 above (or NaN)
       move = move || top[i] != m_ref[i];
     }
     const int v_new = ve > v_ref + 4 ? ve : v_ref;  // or 2^4, for the values' exponent
@@ -512,14 +513,14 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < WARPS; ++k) {
       const float2 st = stats[k * kFewRows + row];
-      if (st.x == -INFINITY) continue;  // it saw no key
+      if (st.x == -INFINITY) continue;  // it saw no key, or none with a weight
       const float g = fast_exp2(st.x - m);
       const float4 x = reinterpret_cast<const float4*>(smem)[(k * kFewRows + row) * kQuads + col];
       sum = fmaf(g, st.y, sum);
       acc.x = fmaf(g, x.x, acc.x), acc.y = fmaf(g, x.y, acc.y), acc.z = fmaf(g, x.z, acc.z), acc.w = fmaf(g, x.w, acc.w);
     }
     if (splits == 1) {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = 1.f / sum;  // 0 / 0 where no logit is above -inf
       reinterpret_cast<uint2*>(chunk_out<D>(p, job, row))[col] =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     } else {

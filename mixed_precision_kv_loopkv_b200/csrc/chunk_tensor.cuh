@@ -171,7 +171,8 @@ __device__ __forceinline__ uint32_t bf16x2_to_half(uint32_t w, float f) {
 // integer (added to 1.5 2^23 and taken off again) and |f| <= 1/2, a cubic for
 // 2^f (fitted at Chebyshev nodes to the least relative error, 7.5e-5, a third of
 // what rounding a weight to fp16 may add), n into the exponent.  -inf and all
-// below -126 give 2^-126, which is 0 as a weight.
+// below -126 give 2^-126, which is 0 as a weight, and so does a NaN: that shows
+// in the row's other columns.
 __device__ __forceinline__ void poly_exp2(uint64_t x2, float& a, float& b) {
   unpack2(x2, a, b);
   const uint64_t x = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
@@ -275,7 +276,7 @@ __device__ __forceinline__ void join_splits(const ChunkAttnParams& p, const Chun
   for (int s = 0; s < splits; ++s) {
     float m, l;
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(peer_addr(stats, s)) : "memory");
-    if (m == -INFINITY) continue;  // it saw no key
+    if (m == -INFINITY) continue;  // it saw no key, or none with a weight
     const float w = fast_exp2(m - top);
     float4 x;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -284,7 +285,7 @@ __device__ __forceinline__ void join_splits(const ChunkAttnParams& p, const Chun
     sum = fmaf(w, l, sum);
     acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = 1.f / sum;  // 0 / 0 where no split had a logit above -inf
   reinterpret_cast<uint2*>(chunk_out<D>(p, job, row))[quad] =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
@@ -801,20 +802,23 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint32_t* x = r + 16 * c;
-        float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-        float b = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
-        a = max3(a, __uint_as_float(x[6]), __uint_as_float(x[7]));
-        b = max3(b, __uint_as_float(x[8]), __uint_as_float(x[9]));
-        a = max3(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
-        b = max3(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
-        a = fmaxf(max3(a, __uint_as_float(x[14]), __uint_as_float(x[15])), b);
-        top = fmaxf(top, a * f[c]);
+        float a = max3_nan(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+        float b = max3_nan(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+        a = max3_nan(a, __uint_as_float(x[6]), __uint_as_float(x[7]));
+        b = max3_nan(b, __uint_as_float(x[8]), __uint_as_float(x[9]));
+        a = max3_nan(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
+        b = max3_nan(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
+        a = max_nan(max3_nan(a, __uint_as_float(x[14]), __uint_as_float(x[15])), b);
+        top = max_nan(top, a * f[c]);
       }
+      // a NaN among the logits, or +inf, whose weight is inf - inf, is the row's
+      // reference: the weights, the sum and with them all of the row are NaN
+      top = top < INFINITY ? top : NAN;
       const int e_top = max(max(ve.x, ve.y), max(ve.z, ve.w));
       // The reference maximum follows the running one only when that is 2^8
       // above it, the value exponent when a block is 2^4 above: weights stay
       // below 2^12, and O is rescaled rarely.
-      const float m_new = top > m_ref + 8.f ? top : m_ref;
+      const float m_new = top <= m_ref + 8.f ? m_ref : top;
       const int v_new = e_top > v_ref + 4 ? e_top : v_ref;
       if (__any_sync(0xffffffffu, m_new != m_ref) || v_new != v_ref) {
         const float shrink = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
@@ -871,7 +875,8 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     if (n > 0 && ok) ok = warp_wait(o_done(m, 1), (n - 1) & 1);
     tc_fence_after();
     if (!idle) {
-      const float f = pow2f(max(min(v_ref, 127), -149)) * (splits == 1 ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
+      // every row sees a key: where no logit is above -inf its weights are 0 / 0
+      const float f = pow2f(max(min(v_ref, 127), -149)) * (splits > 1 ? 1.f : m_ref == -INFINITY ? NAN : 1.f / sum);
       const bool valid = row0 + threadIdx.x < row_end;
       const int local = threadIdx.x;
       __nv_bfloat16* o = chunk_out<D>(p, job, my_row);

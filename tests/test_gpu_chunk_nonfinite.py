@@ -100,3 +100,114 @@ def test_append_of_what_is_not_finite(m, kind, d, turned):
             m.loopkv_quantize_append(want, 0, 0, k_in[:, :n].contiguous(), v[:, :n].contiguous(), table, one)
         have = [a + n for a, n in zip(have, lens)]
         same_bytes(got, want, have)
+
+
+# ---------------------------------------------------------------- attention
+
+
+def attend_any(q, kh, vh, last, sm):
+    """chunk_attend's rows and slack where keys and values need not be finite: a row
+    with a NaN or +inf logit (or -inf alone) is NaN, a logit of -inf has no weight, and
+    a value that is not finite goes into its channel of every row that sees it."""
+    rows, d = q.shape
+    want, slack = np.full((rows, d), np.nan), np.zeros((rows, d))
+    clean = np.where(np.isfinite(vh), vh, 0.0)
+    for i in range(rows):
+        n = last[i] + 1
+        with np.errstate(all="ignore"):
+            s = sm * (kh[:n] @ q[i])
+        if np.isnan(s).any() or s.max() == np.inf or s.max() == -np.inf:
+            continue
+        keep = np.isfinite(s)
+        w, e = CO.chunk_attend(q[i: i + 1], kh[:n][keep], clean[:n][keep], [int(keep.sum()) - 1], sm)
+        with np.errstate(all="ignore"):
+            odd = np.where(np.isfinite(vh[:n]), 0.0, vh[:n])[keep].sum(0)
+        want[i], slack[i] = w[0] + odd, e[0]
+    return want, slack
+
+
+def check(out, want, slack, what):
+    got, fine = host(out).astype(np.float64), np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want)), what
+    odd = ~fine & ~np.isnan(want)
+    assert np.array_equal(got[odd], want[odd]), what
+    assert np.all(np.abs(got - np.where(fine, want, 0))[fine] <= slack[fine]), what
+
+
+def run_case(m, kind, d, T, start, current, spoil, seed=0, sm=0.6, B=8, heads=2, hkv=1):
+    """A chunk behind `start` tokens in each of B sequences; spoil(b, q, k, v, stored) puts
+    into sequence b what is not finite, k and v over stored and current tokens."""
+    n = start if current else start + T
+    k, v = (seeded_bf16((B, start + T, hkv, d), seed + i) for i in range(2))
+    q = seeded_bf16((B, T, heads, d), seed + 2, 0.3)
+    for b in range(B):
+        spoil(b, q[b], k[b], v[b], n)
+    kv, table = cell_for(m, kind, B, hkv, d, max(n, 1), heads, seed)
+    m.loopkv_rope_append(kv, 0, 0, None, None, k[:, :n], v[:, :n], table, ints([0] * B))
+    cur = dict(k_cur=k[:, n:], v_cur=v[:, n:]) if current else {}
+    err = ints([0])
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([start] * B), sm_scale=sm, err_flag=err, **cur)
+    assert int(err) == 0
+    return k, v, q, out
+
+
+def exact_rows(kind, k, v, n, h):
+    """Keys and values of KV head h as they are stood for, all of them finite before."""
+    kh, vh = CO.stored_values(kind, host(k[:n, h]), host(v[:n, h]))
+    return np.vstack([kh, host(k[n:, h]).astype(np.float64)]), np.vstack([vh, host(v[n:, h]).astype(np.float64)])
+
+
+PLACES = [("bf16", 64, 12, 10, False), ("bf16", 128, 140, 10, False), ("q4", 128, 12, 10, False), ("q4", 64, 140, 10, False),
+          ("q2", 128, 140, 10, False), ("q4", 128, 12, 40, True), ("q2", 64, 12, 33, True), ("q4", 128, 140, 40, True),
+          ("bf16", 64, 140, 40, True), ("bf16", 128, 12, 3, True)]
+
+
+@pytest.mark.parametrize("kind,d,T,start,current", PLACES)
+def test_a_nan_key_shows_whatever_its_place(m, kind, d, T, start, current):
+    """Every row that sees a key with a NaN is NaN, at each place of eight."""
+    at = [start + (3 if T < 100 else 121) + b for b in range(8)]     # in the open group of 32
+
+    def spoil(b, q, k, v, n):
+        k[at[b], 0, 5] = NAN
+
+    _, _, _, out = run_case(m, kind, d, T, start, current, spoil)
+    for b in range(8):
+        assert torch.isnan(out[b, at[b] - start:]).all() and not torch.isnan(out[b, : at[b] - start]).any()
+
+
+@pytest.mark.parametrize("kind", ["q4", "bf16"])
+@pytest.mark.parametrize("T,start", [(5, 0), (150, 0), (5, 1500), (150, 1500)])
+def test_queries_that_are_not_finite(m, kind, T, start):
+    """One head's row with a NaN, one with an infinity: those rows are NaN, however
+    the context is split, and no others change."""
+    def spoil(b, q, k, v, n):
+        q[1, 0, 7], q[3, 1, 0], q[T - 1, 1, 3] = NAN, INF, -INF
+        k[:, 0, 3] = k[:, 0, 3].abs() + 0.1      # so that all of that row's logits are -inf
+
+    k, v, q, out = run_case(m, kind, 128, T, start, False, spoil, B=2)
+    for b in range(2):
+        kh, vh = exact_rows(kind, k[b], v[b], start + T, 0)
+        for h in range(2):
+            want, slack = attend_any(host(q[b, :, h]).astype(np.float64), kh, vh, start + np.arange(T), 0.6)
+            bad = {0: {1}, 1: {3, T - 1}}[h]
+            assert {i for i in range(T) if np.isnan(want[i]).any()} == bad
+            check(out[b, :, h], want, slack, (b, h))
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2"])
+@pytest.mark.parametrize("T,start", [(8, 88), (140, 0)])
+def test_a_quantised_key_group_that_is_not_finite(m, kind, T, start):
+    """An infinite key makes its channel's scale infinite: the whole group of 32
+    tokens has no logits, and rows before it are as they were."""
+    def spoil(b, q, k, v, n):
+        k[70, 0, 9] = INF
+
+    k, v, q, out = run_case(m, kind, 128, T, start, False, spoil, seed=3, B=2)
+    for b in range(2):
+        clean = k[b].clone()
+        clean[70, 0, 9] = 0
+        kh, vh = exact_rows(kind, clean, v[b], start + T, 0)
+        kh[64:96, 9] = np.nan
+        for h in range(2):
+            want, slack = attend_any(host(q[b, :, h]).astype(np.float64), kh, vh, start + np.arange(T), 0.6)
+            check(out[b, :, h], want, slack, (b, h))
