@@ -39,8 +39,9 @@ struct FewSmem {
   static constexpr int kRing = WARPS * kFewStages * kGroupBytes;
   static constexpr int kOut = WARPS * kFewRows * D * 4;          // the warps' partial outputs, over the ring
   static constexpr int kMeta = (kRing > kOut ? kRing : kOut);        // each warp: a group's key scales and minima
-  static constexpr int kStats = kMeta + WARPS * D * 4;           // each warp: (max, sum) of 16 rows, value exponent
-  static constexpr int kJoin = kStats + WARPS * (kFewRows * 8 + 16);
+  static constexpr int kStats = kMeta + WARPS * D * 4;           // each warp: (max, sum) of 16 rows
+  static constexpr int kOdd = kStats + WARPS * kFewRows * 8;     // each warp: OddRange
+  static constexpr int kJoin = kOdd + WARPS * 16;
   static constexpr int kJoinStats = kJoin + kFewRows * D * 4;        // the CTA's own result, for its cluster
   static constexpr int kBars = kJoinStats + kFewRows * 8;
   static constexpr int kBytes = kBars + WARPS * kFewStages * 8;
@@ -182,7 +183,8 @@ struct FewWarp {
     return e;
   }
 
-  // Exact rows: row(token of the group) is the key's row or null (zeros).
+  // Exact rows: row(token of the group) is the key's row or null (zeros); the
+  // exponent is that of the finite entries.
   template <typename Row>
   __device__ int exact_logits(Row&& row, float (&s)[4][4]) const {
     uint32_t top = 0;
@@ -192,8 +194,7 @@ struct FewWarp {
       if (src)
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-          const uint4 w = reinterpret_cast<const uint4*>(src + r * (D / 4))[k];
-          top = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(top, w.x), w.y), w.z), w.w);
+          top = abs_max_bf16x8(top, finite_bf16x8(reinterpret_cast<const uint4*>(src + r * (D / 4))[k]));
         }
     }
     const int e = block_exp<kExactTopExp>(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
@@ -267,9 +268,24 @@ struct FewWarp {
     }
   }
 
+  // Zeros in the place of the (scale, min) words in shared memory that are not
+  // finite, which are left to odd_values; whether there were any.  The next copy
+  // into the record comes after.
+  __device__ __noinline__ static bool drop_odd_meta(uint8_t* rec) {
+    constexpr int kWords = kBlock * (D / kGroup);
+    bool any = false;
+    for (int i = threadIdx.x % 32; i < 2 * kWords; i += 32) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(rec + i / kWords * R::kBytes + R::kVMetaOff) + i % kWords;
+      if (odd_meta(*w)) *w = 0u, any = true;
+    }
+    fence_proxy_async_shared();
+    return __any_sync(0xffffffffu, any);
+  }
+
   // (scale, min) words of the thread's tokens (4 r .. of each block) and channels;
-  // tokens from n on are no values.  Returns the exponent of the group's values.
-  __device__ int quant_value_meta(const uint8_t* rec, int n, uint32_t (&meta)[2][4]) const {
+  // tokens from n on are no values.  Returns the bits of the group's largest value,
+  // those of infinity or above where one is not finite.
+  __device__ uint32_t quant_value_meta(const uint8_t* rec, int n, uint32_t (&meta)[2][4]) const {
     const uint8_t* at = rec + R::kVMetaOff + (4 * r * (D / kGroup) + quad * CH / kGroup) * 4;
     float top = 0.f;
 #pragma unroll
@@ -286,9 +302,9 @@ struct FewWarp {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float s = bf16_lo(meta[i >> 2][i & 3]), mn = bf16_hi(meta[i >> 2][i & 3]);
-      top = max3(top, fabsf(mn), fabsf(fmaf(s, kTop, mn)));
+      top = max3_nan(top, fabsf(mn), fabsf(fmaf(s, kTop, mn)));
     }
-    return block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   }
 
   __device__ void quant_output(const uint8_t* rec, const uint32_t (&meta)[2][4], int e, const uint32_t (&a)[2][4]) {
@@ -343,18 +359,21 @@ struct FewWarp {
   }
 
   template <typename Row>
-  __device__ int exact_value_exp(Row&& row) const {
+  __device__ int exact_value_exp(Row&& row, bool& odd) const {
     uint32_t top = 0;
+    bool some = false;
 #pragma unroll 1
     for (int t = 0; t < 8; ++t) {
       const __nv_bfloat16* src = row((t >> 2) * kBlock + 4 * r + (t & 3));
       if (src)
 #pragma unroll
         for (int k = 0; k < CH / 8; ++k) {
-          const uint4 w = reinterpret_cast<const uint4*>(src + quad * CH)[k];
-          top = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(top, w.x), w.y), w.z), w.w);
+          const uint4 w = reinterpret_cast<const uint4*>(src + quad * CH)[k], f = finite_bf16x8(w);
+          some = some || w.x != f.x || w.y != f.y || w.z != f.z || w.w != f.w;
+          top = abs_max_bf16x8(top, f);
         }
     }
+    odd = __any_sync(0xffffffffu, some);
     return block_exp(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
   }
 
@@ -370,7 +389,7 @@ struct FewWarp {
         for (int t = 0; t < 4; ++t) {
           const __nv_bfloat16* src = row(blk * kBlock + 4 * r + t);
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (src) v = reinterpret_cast<const uint4*>(src + quad * CH)[k];
+          if (src) v = finite_bf16x8(reinterpret_cast<const uint4*>(src + quad * CH)[k]);
           w[t][0] = v.x, w[t][1] = v.y, w[t][2] = v.z, w[t][3] = v.w;
         }
 #pragma unroll
@@ -399,7 +418,7 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
   job.hk = unit % p.Hkv;
   job.b = unit / p.Hkv;
   if (!chunk_job<D>(p, job, 0, kFewRows, job.hk == 0 && rank == 0, rank == 0)) return;
-  const int rows = job.len << p.g_log2;
+  const int job_rows = job.len << p.g_log2;
   // groups over the stored tokens, then one over the chunk's own (at most 16) rows
   const int stored_groups = (job.stored + kGroup - 1) / kGroup, groups = stored_groups + (job.current ? 1 : 0);
   const int first = static_cast<int>(static_cast<int64_t>(groups) * rank / splits);
@@ -408,7 +427,9 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
 
   // this warp's ring: group i of its own in stage i % stages
   const uint32_t ring = sbase + warp * kFewStages * L::kGroupBytes, bar = sbase + L::kBars + warp * kFewStages * 8;
+  const uint32_t odd_at = sbase + L::kOdd + warp * 16;
   if (lane == 0) {
+    *reinterpret_cast<OddRange*>(smem + L::kOdd + warp * 16) = OddRange{INT32_MAX, 0};
     for (int s = 0; s < kFewStages; ++s) mbar_init(bar + 8 * s, 1);
     fence_mbar_init();
   }
@@ -440,8 +461,8 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
   for (int i = 0; i < kFewStages - 1; ++i) issue(i);
 
   W w(p, job, lane);
-  w.load_queries(rows);
-  const int token[2] = {min(w.quad, rows - 1) >> p.g_log2, min(w.quad + 8, rows - 1) >> p.g_log2};
+  w.load_queries(job_rows);
+  const int token[2] = {min(w.quad, job_rows - 1) >> p.g_log2, min(w.quad + 8, job_rows - 1) >> p.g_log2};
   const uint32_t meta = sbase + L::kMeta + warp * D * 4;
   bool ok = true;
 #pragma unroll 1
@@ -449,32 +470,42 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
     const int g = first + warp + i * WARPS, t0 = g * kGroup, s = i % kFewStages;
     __syncwarp();      // the stage that comes next has been read by all
     issue(i + kFewStages - 1);
-    float logit[4][4] = {};
     uint32_t a[2][4];
     if (g >= stored_groups) {
+      float logit[4][4] = {};
       // the chunk's own rows, exactly
       auto key = [&](int t) { return t < job.len ? row_at(p.k_cur, job.b, t, job.hk) : nullptr; };
       auto value = [&](int t) { return t < job.len ? row_at(p.v_cur, job.b, t, job.hk) : nullptr; };
       const int lim[2] = {token[0] + 1, token[1] + 1};
-      const int ke = w.exact_logits(key, logit), ve = w.exact_value_exp(value);
+      bool some;
+      const int ke = w.exact_logits(key, logit), ve = w.exact_value_exp(value, some);
+      if (some && lane == 0) note_odd_keys(odd_at, t0, kGroup);
       w.weights(logit, ke, ve, lim, a);
       w.exact_output(value, ve, a);
       continue;
     }
     ok = warp_wait(bar + 8 * s, (i / kFewStages) & 1);
     if (!ok) break;
-    const uint8_t* rec = smem + (warp * kFewStages + s) * L::kGroupBytes;
+    uint8_t* rec = smem + (warp * kFewStages + s) * L::kGroupBytes;
     const int lim[2] = {(job.current ? job.stored : job.start + token[0] + 1) - t0,
                         (job.current ? job.stored : job.start + token[1] + 1) - t0};
+    float logit[4][4];
+    uint32_t value_meta[2][4], top;
     int ke;
-    if (t0 + kGroup <= job.stored) {
-      ke = w.quant_logits(rec, meta, logit);
-    } else {  // the open group's keys
-      const __nv_bfloat16* res = p.residual + (static_cast<size_t>(job.b) * p.Hkv + job.hk) * kGroup * D;
-      ke = w.exact_logits([&](int t) { return t0 + t < job.stored ? res + t * D : nullptr; }, logit);
-    }
-    uint32_t value_meta[2][4];
-    const int ve = w.quant_value_meta(rec, job.stored - t0, value_meta);
+    do {  // once more where values that are not finite were dropped
+#pragma unroll
+      for (int n = 0; n < 4; ++n) logit[n][0] = logit[n][1] = logit[n][2] = logit[n][3] = 0.f;
+      if (t0 + kGroup <= job.stored) {
+        ke = w.quant_logits(rec, meta, logit);
+      } else {  // the open group's keys
+        const __nv_bfloat16* res = p.residual + (static_cast<size_t>(job.b) * p.Hkv + job.hk) * kGroup * D;
+        ke = w.exact_logits([&](int t) { return t0 + t < job.stored ? res + t * D : nullptr; }, logit);
+      }
+      top = w.quant_value_meta(rec, job.stored - t0, value_meta);
+      if (top < 0x7F800000u) break;
+      if (lane == 0) note_odd_keys(odd_at, t0, kGroup);
+    } while (w.drop_odd_meta(rec));
+    const int ve = block_exp(top);
     w.weights(logit, ke, ve, lim, a);
     w.quant_output(rec, value_meta, ve, a);
   }
@@ -502,6 +533,22 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
     stats[warp * kFewRows + w.quad] = make_float2(w.m_ref[0], w.sum[0]);
     stats[warp * kFewRows + w.quad + 8] = make_float2(w.m_ref[1], w.sum[1]);
   }
+  // what follows is worked out anew, so as not to hold it over the groups
+  ChunkJob at;
+  at.hk = (cta_id_x() / splits) % p.Hkv;
+  at.b = (cta_id_x() / splits) / p.Hkv;
+  const int tokens = p.chunk.new_lens ? p.chunk.new_lens[at.b] : p.chunk.T, rows = tokens << p.g_log2;
+  __syncwarp();
+  const OddRange odd = *reinterpret_cast<const OddRange*>(smem + L::kOdd + warp * 16);
+  if (ok && odd.first < odd.end) {
+    const int start = p.chunk.start_pos[at.b], stored = start + (p.k_cur.p ? 0 : tokens);
+#pragma unroll 1
+    for (int i = lane; i < rows * D; i += 32) {
+      const int t = (i / D) >> p.g_log2;
+      out[i] += odd_values<KIND, D>(p, at.b, at.hk, p.k_cur.p ? start : start + t + 1, t + 1,
+                                    (stored + kGroup - 1) / kGroup * kGroup, odd, i % D);
+    }
+  }
   __syncthreads();
   constexpr int kQuads = D / 4;
   float4* join = reinterpret_cast<float4*>(smem + L::kJoin);
@@ -521,7 +568,7 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
     }
     if (splits == 1) {
       const float inv = 1.f / sum;  // 0 / 0 where no logit is above -inf
-      reinterpret_cast<uint2*>(chunk_out<D>(p, job, row))[col] =
+      reinterpret_cast<uint2*>(chunk_out<D>(p, at, row))[col] =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     } else {
       join[i] = acc;
@@ -529,11 +576,12 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
     }
   }
   if (splits == 1) return;
+  const int rank_again = cta_id_x() % splits;
   cluster_sync_all();
   for (int i = threadIdx.x; i < rows * kQuads; i += kThreads) {
-    if (i / 32 % splits != rank) continue;
+    if (i / 32 % splits != rank_again) continue;
     const int row = i / kQuads;
-    join_splits<D>(p, job, row, i % kQuads, splits, sbase + L::kJoinStats + row * 8, sbase + L::kJoin + i * 16);
+    join_splits<D>(p, at, row, i % kQuads, splits, sbase + L::kJoinStats + row * 8, sbase + L::kJoin + i * 16);
   }
   cluster_sync_all();
 }

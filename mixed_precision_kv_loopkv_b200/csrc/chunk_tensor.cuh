@@ -66,7 +66,8 @@ struct ChunkSmem {
   static constexpr int kBars = kStats + MT * 128 * 8;
   static constexpr int kBarCount = 9 + 2 * 6;
   static constexpr int kTmem = kBars + kBarCount * 8;
-  static constexpr int kBytes = kTmem + 8;
+  static constexpr int kOdd = kTmem + 8;             // OddRange
+  static constexpr int kBytes = kOdd + 8;
   static constexpr int kPartial = kK;                // fp32 partial O over the stages: MT 128 D 4 = MT kTile 2 <= 4 kTile
 };
 
@@ -162,6 +163,19 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
 
 __device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
 
+// bf16 pair without what is not finite.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  return w & ~__vcmpgtu2(w & 0x7FFF7FFFu, 0x7F7F7F7Fu);
+}
+__device__ __forceinline__ uint4 finite_bf16x8(const uint4& w) {
+  return make_uint4(finite_bf16x2(w.x), finite_bf16x2(w.y), finite_bf16x2(w.z), finite_bf16x2(w.w));
+}
+__device__ __forceinline__ uint32_t abs_max_bf16x8(uint32_t m, const uint4& w) {
+  return abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(m, w.x), w.y), w.z), w.w);
+}
+// (scale, min) that stands for values which are not all finite.
+__device__ __forceinline__ bool odd_meta(uint32_t w) { return finite_bf16x2(w) != w; }
+
 // bf16 pair times f (a power of two) as fp16 pair.
 __device__ __forceinline__ uint32_t bf16x2_to_half(uint32_t w, float f) {
   return half2_bits(__floats2half2_rn(bf16_lo(w) * f, bf16_hi(w) * f));
@@ -200,6 +214,55 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     } while (!done && global_timer_ns() - t0 <= kWaitTimeoutNs);
   }
   return __all_sync(0xffffffffu, done);
+}
+
+// Values that are not finite.  A weight of 0 times one would be NaN in rows that
+// must not see it, so they enter the products as 0; where the blocks that hold
+// them lie is noted here, and each row adds those that it sees at the end.  Keys
+// count on: the stored tokens' tiles (groups), then the current rows'.
+struct OddRange {
+  int first, end;  // none: first >= end
+};
+
+// One thread's note of count keys from `first` on, to the range at a shared address.
+__device__ __forceinline__ void note_odd_keys(uint32_t odd_at, int first, int count) {
+  asm volatile("red.shared::cta.min.s32 [%0], %1;" ::"r"(odd_at), "r"(first) : "memory");
+  asm volatile("red.shared::cta.max.s32 [%0], %1;" ::"r"(odd_at + 4), "r"(first + count) : "memory");
+}
+
+// Value c of stored token t, as read_tokens gives it but not rounded.
+template <int KIND, int D>
+__device__ float stored_value(const ChunkAttnParams& p, int b, int hk, int t, int c) {
+  using R = Rec<KIND, D>;
+  const int phys = p.block_table[static_cast<size_t>(b) * p.max_blocks + t / kBlock], row = t % kBlock;
+  const uint8_t* rec = p.arena + (static_cast<size_t>(phys) * p.Hkv + hk) * R::kBytes;
+  if constexpr (KIND == LOOPKV_CELL_BF16) {
+    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rec + R::kBfV)[row * D + c]);
+  } else {
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(rec + R::kVMetaOff + (row * (D / kGroup) + c / kGroup) * 4);
+    uint32_t code = (rec[R::kVHi + c / 4 * kBlock + row] >> (2 * (c % 4))) & 3u;
+    if constexpr (KIND == LOOPKV_CELL_Q4) code = code << 2 | ((rec[R::kQ4VLo + row * R::kRow + c / 4] >> (2 * (c % 4))) & 3u);
+    return fmaf(bf16_lo(m), static_cast<float>(code), bf16_hi(m));
+  }
+}
+
+// What those of odd's keys add to channel c of a row that sees `stored` stored
+// tokens and `current` current rows: 0, an infinity or NaN.  Current rows count
+// from key0 on.
+template <int KIND, int D>
+__device__ __forceinline__ float odd_values(const ChunkAttnParams& p, int b, int hk, int stored, int current, int key0,
+                                         OddRange odd, int c) {
+  float sum = 0.f;
+  for (int i = odd.first; i < odd.end; ++i) {
+    float v = 0.f;
+    if (i < key0) {
+      if (i < stored) v = stored_value<KIND, D>(p, b, hk, i, c);
+    } else if (i - key0 < current) {
+      v = __bfloat162float(row_at(p.v_cur, b, i - key0, hk)[c]);
+    }
+    if (!isfinite(v)) sum += v;
+  }
+  return sum;
 }
 
 // What the CTA works on.
@@ -309,6 +372,7 @@ struct BlockLoader {
 
   const ChunkAttnParams& p;
   const ChunkJob& job;
+  uint32_t odd_at;       // the CTA's OddRange
   int block, lane, c16, sub;
   int key0;              // first of the thread's tokens as a key: key0 + SUBS i
   int flip;              // its tokens as a value: sub KPL + (k ^ flip)
@@ -316,8 +380,8 @@ struct BlockLoader {
 
   // Where eight neighbouring threads would write rows of the same parity to
   // the same banks, half of them take the other row of a pair.
-  __device__ BlockLoader(const ChunkAttnParams& p, const ChunkJob& job, int block, int lane)
-      : p(p), job(job), block(block), lane(lane), c16(lane % C16), sub(lane / C16) {
+  __device__ BlockLoader(const ChunkAttnParams& p, const ChunkJob& job, uint32_t odd_at, int block, int lane)
+      : p(p), job(job), odd_at(odd_at), block(block), lane(lane), c16(lane % C16), sub(lane / C16) {
     key0 = D == 128 ? sub ^ (c16 >> 2) : sub;
     flip = D == 128 ? c16 >> 2 : sub & 1;
     key_at = swz(block * kBlock + key0, 2 * c16);
@@ -401,8 +465,10 @@ struct BlockLoader {
   }
 
   // Exact bf16 rows into the tile; row(token) is the token's row or null (zeros).
+  // The exponent is that of the finite entries: others must not take theirs from
+  // the rest of the block, which rows before them see.
   template <bool KEYS, typename Row>
-  __device__ int store_exact(uint32_t tile_base, Row&& row) const {
+  __device__ int store_exact(int tile, uint32_t tile_base, Row&& row) const {
     uint4 w[KPL][2];
     uint32_t top = 0;
 #pragma unroll
@@ -415,13 +481,22 @@ struct BlockLoader {
       }
     }
 #pragma unroll
-    for (int k = 0; k < KPL; ++k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        top = abs_max_bf16x2(abs_max_bf16x2(top, w[k][j].x), w[k][j].y);
-        top = abs_max_bf16x2(abs_max_bf16x2(top, w[k][j].z), w[k][j].w);
-      }
+    for (int k = 0; k < KPL; ++k) top = abs_max_bf16x8(abs_max_bf16x8(top, w[k][0]), w[k][1]);
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    if (top >= 0x7F80u) {
+      asm volatile("");
+      top = 0;
+#pragma unroll
+      for (int k = 0; k < KPL; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint4 x = finite_bf16x8(w[k][j]);
+          top = abs_max_bf16x8(top, x);
+          if constexpr (!KEYS) w[k][j] = x;
+        }
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+      if (!KEYS && lane == 0) note_odd_keys(odd_at, token0(tile), kBlock);
+    }
     const int e = block_exp<KEYS || !kQuant ? kExactTopExp : kTopExp>(top << 16);
     const float f = pow2f(-e);
 #pragma unroll
@@ -442,14 +517,14 @@ struct BlockLoader {
     const int t0 = token0(tile);
     if (tile >= job.stored_tiles) {
       const int c0 = t0 - job.stored_tiles * kTileKeys;
-      return store_exact<true>(tile_base, [&](int t) {
+      return store_exact<true>(tile, tile_base, [&](int t) {
         return c0 + t < job.len ? row_at(p.k_cur, job.b, c0 + t, job.hk) : nullptr;
       });
     }
     if constexpr (kQuant) {
       if (!full(t0)) {
         const __nv_bfloat16* res = p.residual + (static_cast<size_t>(job.b) * p.Hkv + job.hk) * kGroup * D;
-        return store_exact<true>(tile_base, [&](int t) {
+        return store_exact<true>(tile, tile_base, [&](int t) {
           return t0 + t < job.stored ? res + ((t0 + t) % kGroup) * D : nullptr;
         });
       }
@@ -498,32 +573,43 @@ struct BlockLoader {
       return e;
     } else {
       const uint8_t* rec = record(id.x);
-      return store_exact<true>(tile_base, [&](int t) {
+      return store_exact<true>(tile, tile_base, [&](int t) {
         return t0 + t < job.stored ? reinterpret_cast<const __nv_bfloat16*>(rec + R::kBfK) + t * D : nullptr;
       });
     }
   }
 
   // Values of the block into the tile; returns their exponent.
-  __device__ int store(int tile, int2 id, const RawValues& r, uint32_t tile_base) const {
+  __device__ int store(int tile, int2 id, RawValues& r, uint32_t tile_base) const {
     const int t0 = token0(tile);
     if (tile >= job.stored_tiles) {
       const int c0 = t0 - job.stored_tiles * kTileKeys;
-      return store_exact<false>(tile_base, [&](int t) {
+      return store_exact<false>(tile, tile_base, [&](int t) {
         return c0 + t < job.len ? row_at(p.v_cur, job.b, c0 + t, job.hk) : nullptr;
       });
     }
     if constexpr (kQuant) {
       constexpr float kTop = kSplit ? 15.f : 3.f;
-      float s[KPL], mn[KPL], top = 0.f;
+      float s[KPL], mn[KPL];
+      uint32_t top_bits;
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        float top = 0.f;
 #pragma unroll
-      for (int k = 0; k < KPL; ++k) {
-        // what lies behind the last token is no value
-        const uint32_t w = t0 + value_token(k) < job.stored ? r.meta[k] : 0u;
-        s[k] = bf16_lo(w), mn[k] = bf16_hi(w);
-        top = fmaxf(top, fmaxf(fabsf(mn[k]), fabsf(fmaf(s[k], kTop, mn[k]))));
+        for (int k = 0; k < KPL; ++k) {
+          // what lies behind the last token is no value
+          const uint32_t w = t0 + value_token(k) < job.stored ? r.meta[k] : 0u;
+          s[k] = bf16_lo(w), mn[k] = bf16_hi(w);
+          top = max3_nan(top, fabsf(mn[k]), fabsf(fmaf(s[k], kTop, mn[k])));
+        }
+        top_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if (top_bits < 0x7F800000u || again) break;
+#pragma unroll
+        for (int k = 0; k < KPL; ++k)
+          if (odd_meta(r.meta[k])) r.meta[k] = 0u;
+        if (lane == 0) note_odd_keys(odd_at, t0, kBlock);
       }
-      const int e = block_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      const int e = block_exp(top_bits);
       const float fs = block_unit<kSplit ? 24 : 22>(e), f = fs * (kSplit ? 0x1p-24f : 0x1p-22f);
 #pragma unroll
       for (int k = 0; k < KPL; ++k) {
@@ -538,7 +624,7 @@ struct BlockLoader {
       return e;
     } else {
       const uint8_t* rec = record(id.x);
-      return store_exact<false>(tile_base, [&](int t) {
+      return store_exact<false>(tile, tile_base, [&](int t) {
         return t0 + t < job.stored ? reinterpret_cast<const __nv_bfloat16*>(rec + R::kBfV) + t * D : nullptr;
       });
     }
@@ -587,6 +673,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
   auto o_done = [&](int m, int buf) { return bars + 136 + 16 * m + 8 * buf; };  // and are in O
   float* k_exp = reinterpret_cast<float*>(smem + L::kKExp);
   int* v_exp = reinterpret_cast<int*>(smem + L::kVExp);
+  OddRange* odd = reinterpret_cast<OddRange*>(smem + L::kOdd);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -605,6 +692,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       }
     }
     fence_mbar_init();
+    *odd = OddRange{INT32_MAX, 0};
   }
   if (warp == kIssueWarp) tmem_alloc<kTmemCols>(sbase + L::kTmem);
   tc_fence_before();
@@ -631,7 +719,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     // ------------------------------------------------------------ dequantise
     set_max_registers<ChunkRegs<MT>::kDequant, ChunkRegs<MT>::kLaunch>();
     const int block = warp - kSoftmaxWarps;
-    const BlockLoader<KIND, D> loader(p, job, block, lane);
+    const BlockLoader<KIND, D> loader(p, job, sbase + L::kOdd, block, lane);
     typename BlockLoader<KIND, D>::RawKeys keys = {};
     typename BlockLoader<KIND, D>::RawValues values = {};
     // The records' bytes come one tile ahead, each part into the registers that
@@ -874,12 +962,18 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     // ------------------------------------------------------------ results
     if (n > 0 && ok) ok = warp_wait(o_done(m, 1), (n - 1) & 1);
     tc_fence_after();
-    if (!idle) {
+    // where the rows lie is worked out anew, so as not to hold it over the steps
+    const uint32_t unit_again = cta_id_x() / splits;
+    const int local = threadIdx.x, row = (row_tiles - 1 - static_cast<int>(unit_again % row_tiles)) * kRows + local;
+    ChunkJob at;
+    at.hk = (unit_again / row_tiles) % p.Hkv;
+    at.b = unit_again / row_tiles / p.Hkv;
+    const int rows = (p.chunk.new_lens ? p.chunk.new_lens[at.b] : p.chunk.T) << p.g_log2;
+    if (row - lane < rows) {
       // every row sees a key: where no logit is above -inf its weights are 0 / 0
       const float f = pow2f(max(min(v_ref, 127), -149)) * (splits > 1 ? 1.f : m_ref == -INFINITY ? NAN : 1.f / sum);
-      const bool valid = row0 + threadIdx.x < row_end;
-      const int local = threadIdx.x;
-      __nv_bfloat16* o = chunk_out<D>(p, job, my_row);
+      const bool valid = row < rows;
+      __nv_bfloat16* o = chunk_out<D>(p, at, min(row, rows - 1));
       if (splits > 1) reinterpret_cast<float2*>(smem + L::kStats)[local] = make_float2(m_ref, sum);
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
@@ -909,6 +1003,20 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
                 make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
         }
       }
+      // (all blocks' notes came before the last values' arrival)
+      const OddRange found{*reinterpret_cast<volatile int*>(&odd->first), *reinterpret_cast<volatile int*>(&odd->end)};
+      if (ok && valid && found.first < found.end) {
+        const int token = row >> p.g_log2, see = p.chunk.start_pos[at.b] + (p.k_cur.p ? 0 : token + 1);
+#pragma unroll 1
+        for (int c = 0; c < D; ++c) {
+          const float v = odd_values<KIND, D>(p, at.b, at.hk, see, token + 1, job.stored_tiles * kTileKeys, found, c);
+          if (v == 0.f) continue;
+          if (splits == 1)
+            o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + v);
+          else
+            reinterpret_cast<float*>(smem + L::kPartial + local * D * 4 + (((c / 4) ^ (local & (D / 4 - 1))) << 4))[c % 4] += v;
+        }
+      }
     }
   }
   if (!ok && lane == 0) flag_error(p.chunk.err, LOOPKV_DEVERR_TIMEOUT);
@@ -924,10 +1032,17 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     const uint32_t stats = sbase + L::kStats, partial = sbase + L::kPartial;
     constexpr int kQuads = D / 4, kRowsPerWarp = 32 / kQuads;
     const int quad = lane % kQuads;
+    const uint32_t unit_again = cta_id_x() / splits;
+    const int first = (row_tiles - 1 - static_cast<int>(unit_again % row_tiles)) * kRows;
+    ChunkJob at;
+    at.hk = (unit_again / row_tiles) % p.Hkv;
+    at.b = unit_again / row_tiles / p.Hkv;
+    const int rows = min(((p.chunk.new_lens ? p.chunk.new_lens[at.b] : p.chunk.T) << p.g_log2) - first, kRows);
+    const int rank = cta_id_x() % splits;
     for (int i = warp * kRowsPerWarp + lane / kQuads;; i += kSoftmaxWarps * kRowsPerWarp) {
       const int row = i * splits + rank;
-      if (row0 + row >= row_end) break;
-      join_splits<D>(p, job, row0 + row, quad, splits, stats + row * 8,
+      if (row >= rows) break;
+      join_splits<D>(p, at, first + row, quad, splits, stats + row * 8,
                      partial + row * D * 4 + ((quad ^ (row & (kQuads - 1))) << 4));
     }
   }

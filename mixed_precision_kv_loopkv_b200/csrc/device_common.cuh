@@ -126,8 +126,13 @@ __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
-// blockIdx.y read afresh (not merged with earlier reads, so that it need not
-// stay in a register in between)
+// blockIdx.x and .y read afresh (not merged with earlier reads, so that they need
+// not stay in a register in between)
+__device__ __forceinline__ int cta_id_x() {
+  int r;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(r));
+  return r;
+}
 __device__ __forceinline__ int cta_id_y() {
   int r;
   asm volatile("mov.u32 %0, %%ctaid.y;" : "=r"(r));

@@ -175,6 +175,30 @@ def test_a_nan_key_shows_whatever_its_place(m, kind, d, T, start, current):
         assert torch.isnan(out[b, at[b] - start:]).all() and not torch.isnan(out[b, : at[b] - start]).any()
 
 
+@pytest.mark.parametrize("kind,d,T,start,current", PLACES)
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_keys_that_are_not_finite(m, kind, d, T, start, current, value):
+    """An exact key with one such entry, at each place of eight: rows before it
+    are as without it, rows that see it are NaN, or have no weight for it where
+    its logit is -inf."""
+    B = 8
+    at = [start + (3 if T < 100 else 121) + b for b in range(B)]     # in the open group of 32
+
+    def spoil(b, q, k, v, n):
+        k[at[b], 0, 5] = value
+
+    k, v, q, out = run_case(m, kind, d, T, start, current, spoil, B=B)
+    n = start if current else start + T
+    for b in range(B):
+        clean = k[b].clone()
+        clean[at[b], 0, 5] = 0
+        kh, vh = exact_rows(kind, clean, v[b], n, 0)
+        kh[at[b], 5] = value
+        for h in range(2):
+            want, slack = attend_any(host(q[b, :, h]).astype(np.float64), kh, vh, start + np.arange(T), 0.6)
+            check(out[b, :, h], want, slack, (b, h))
+
+
 @pytest.mark.parametrize("kind", ["q4", "bf16"])
 @pytest.mark.parametrize("T,start", [(5, 0), (150, 0), (5, 1500), (150, 1500)])
 def test_queries_that_are_not_finite(m, kind, T, start):
@@ -191,6 +215,58 @@ def test_queries_that_are_not_finite(m, kind, T, start):
             want, slack = attend_any(host(q[b, :, h]).astype(np.float64), kh, vh, start + np.arange(T), 0.6)
             bad = {0: {1}, 1: {3, T - 1}}[h]
             assert {i for i in range(T) if np.isnan(want[i]).any()} == bad
+            check(out[b, :, h], want, slack, (b, h))
+
+
+@pytest.mark.parametrize("kind,d,T,start,current", PLACES)
+def test_values_that_are_not_finite(m, kind, d, T, start, current):
+    """A value's infinity or NaN reaches its channel of the rows that see it, and
+    nothing else; two infinities of both signs meet as NaN."""
+    B, n = 8, start if current else start + T
+    odd = {}
+
+    def spoil(b, q, k, v, n):
+        j = start + (2 if T < 100 else 118) + b
+        odd[b] = [(j, 1, [INF, -INF, NAN, INF][b % 4]), (j + 1, 40, -INF), (j + 2, 40, INF), (min(b, start - 1), 2, NAN)]
+        for t, c, x in odd[b]:
+            if t < n and kind != "bf16":           # a quantised group of 32 channels goes as a whole
+                v[t, 0, c // 32 * 32: c // 32 * 32 + 32] = x
+            else:
+                v[t, 0, c] = x
+
+    k, v, q, out = run_case(m, kind, d, T, start, current, spoil, seed=5, B=B)
+    for b in range(B):
+        clean = torch.where(torch.isfinite(v[b]), v[b], torch.zeros_like(v[b]))
+        kh, vh = exact_rows(kind, k[b], clean, n, 0)
+        for t, c, x in odd[b]:
+            if t < n and kind != "bf16":
+                vh[t, c // 32 * 32: c // 32 * 32 + 32] = np.nan     # inf times the code 0
+            else:
+                vh[t, c] = x
+        for h in range(2):
+            want, slack = attend_any(host(q[b, :, h]).astype(np.float64), kh, vh, start + np.arange(T), 0.6)
+            check(out[b, :, h], want, slack, (b, h))
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2", "bf16"])
+@pytest.mark.parametrize("T", [9, 200])
+def test_values_that_are_not_finite_in_a_split_context(m, kind, T):
+    """The same with the context split over CTAs, and with whole rows of values."""
+    start, d = 1400, 128
+    places = [100, 101, 1403, start + T - 3]
+
+    def spoil(b, q, k, v, n):
+        v[places[0], 0, 32:64], v[places[1], 0, 64:96] = INF, NAN
+        v[places[2], 0], v[places[3], 0] = NAN, -INF
+
+    k, v, q, out = run_case(m, kind, d, T, start, False, spoil, seed=9, B=2)
+    for b in range(2):
+        clean = torch.where(torch.isfinite(v[b]), v[b], torch.zeros_like(v[b]))
+        kh, vh = exact_rows(kind, k[b], clean, start + T, 0)
+        raw = host(v[b, :, 0]).astype(np.float64)
+        vh = np.where(np.isfinite(raw), vh, raw if kind == "bf16" else np.nan)
+        for h in range(2):
+            want, slack = attend_any(host(q[b, :, h]).astype(np.float64), kh, vh, start + np.arange(T), 0.6)
             check(out[b, :, h], want, slack, (b, h))
 
 
