@@ -134,8 +134,12 @@ LOOPKV_API loopkv_status loopkv_read_tokens(const loopkv_config* cfg, const loop
  * decoding has nothing to save here (as tau = 0 there).  Softmax weights and
  * dequantised rows enter the tensor cores in fp16 (11 bits) under powers of two
  * that follow the data, a block of 16 (or group of 32) tokens at a time; sums
- * and statistics are fp32.  Entries less than 2^-8 of the largest of their
- * block lose bits by the same factor (exact keys, and bf16 cells: 2^-22).
+ * and statistics are fp32.  Entries less than 2^-8 of the largest finite one of
+ * their block, whether the row sees that or not, lose bits by the same factor
+ * (exact keys, and bf16 cells: 2^-22); between blocks a row's precision follows
+ * what it sees and weighs.  A row with a logit of NaN or +infinity, or none above
+ * -infinity, is NaN; a value that is not finite shows in its channel of the rows
+ * that see it, and in no others.
  *   q            : rows of num_heads heads (queries already rotated)
  *   k_cur, v_cur : optional rows of num_kv_heads heads (both or neither)
  *   max_seq_len  : host upper bound of the stored tokens; 0: the block table's

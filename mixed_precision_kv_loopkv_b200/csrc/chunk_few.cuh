@@ -75,11 +75,12 @@ struct FewWarp {
   uint32_t q[STEPS][4];
   float row_scale[2];          // rows quad, quad + 8
   float m_ref[2], sum[2];
-  int v_ref;
+  float v_ref[2];
   float o[CH][4];
 
   __device__ FewWarp(const ChunkAttnParams& p, const ChunkJob& job, int lane)
-      : p(p), job(job), lane(lane), quad(lane >> 2), r(lane & 3), v_ref(-1000) {
+      : p(p), job(job), lane(lane), quad(lane >> 2), r(lane & 3) {
+    v_ref[0] = v_ref[1] = kNoValueRef;
     m_ref[0] = m_ref[1] = -INFINITY;
     sum[0] = sum[1] = 0.f;
 #pragma unroll
@@ -213,7 +214,7 @@ struct FewWarp {
     return e;
   }
 
-  // Logits to weights, in place: p 2^(ve - v_ref) as fp16 pairs a[block][4], the
+  // Logits to weights, in place: 2^(logit - m_ref) 2^(ve - v_ref) as fp16 pairs a[block][4], the
   // products' left operand.  lim[i]: keys of the group that row quad + 8 i sees.
   __device__ void weights(float (&s)[4][4], int ke, int ve, const int (&lim)[2], uint32_t (&a)[2][4]) {
     const float k = block_scale(ke);
@@ -226,6 +227,7 @@ struct FewWarp {
         for (int c = 0; c < 4; ++c)
           if ((n >> 1) * kBlock + few_key(2 * r + (c & 1), n & 1) >= lim[c >> 1]) s[n][c] = -INFINITY;
     }
+    const float value_exp = static_cast<float>(ve);
     float f[2], top[2];
     bool move = false;
 #pragma unroll
@@ -234,29 +236,27 @@ struct FewWarp {
       float t = max_nan(max3_nan(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), max3_nan(s[1][2 * i + 1], s[2][2 * i], s[2][2 * i + 1]));
       t = max3_nan(t, s[3][2 * i], s[3][2 * i + 1]) * f[i];
       t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      t = t < INFINITY ? t : NAN;                   // +inf: its weight is inf - inf
-      top[i] = t <= m_ref[i] + 8.f ? m_ref[i] : t;  // follow only what is 2^8 above (or NaN)
-      move = move || top[i] != m_ref[i];
+      top[i] = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      move = move || refs_move(m_ref[i], v_ref[i], top[i], top[i] + value_exp);
     }
-    const int v_new = ve > v_ref + 4 ? ve : v_ref;  // or 2^4, for the values' exponent
-    if (__any_sync(0xffffffffu, move) || v_new != v_ref) {
-      const float g = pow2f(max(v_ref - v_new, -149));
+    if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float shrink = top[i] == m_ref[i] ? 1.f : fast_exp2(m_ref[i] - top[i]);
-        sum[i] *= shrink;
-        m_ref[i] = top[i];
+        const float t = top[i] < INFINITY ? top[i] : NAN;    // +inf: its weight is inf - inf
+        const float m_new = t <= m_ref[i] + kLogitAbove ? m_ref[i] : t;
+        const float v_new = value_ref(v_ref[i], m_ref[i], m_new, t - m_new + value_exp);
+        const float shrink = m_new == m_ref[i] ? 0.f : m_ref[i] - m_new, g = fast_exp2(shrink + (v_ref[i] - v_new));
+        sum[i] *= fast_exp2(shrink);
+        m_ref[i] = m_new;
+        v_ref[i] = v_new;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) o[c][2 * i] *= shrink * g, o[c][2 * i + 1] *= shrink * g;
+        for (int c = 0; c < CH; ++c) o[c][2 * i] *= g, o[c][2 * i + 1] *= g;
       }
-      v_ref = v_new;
     }
-    const int de = max(ve - v_ref, kLeastShift);    // at most 4
-    const float back = __int_as_float((127 - de) << 23);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float off = static_cast<float>(de) - (m_ref[i] == -INFINITY ? 0.f : m_ref[i]);
+      const float de = fmaxf(value_exp - v_ref[i], kLeastShift);
+      const float off = de - (m_ref[i] == -INFINITY ? 0.f : m_ref[i]);
       float part = 0.f;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
@@ -264,22 +264,8 @@ struct FewWarp {
         part += x + y;
         a[n >> 1][2 * (n & 1) + i] = half2_bits(__floats2half2_rn(x, y));
       }
-      sum[i] = fmaf(part, back, sum[i]);            // this thread's columns; the quad's are added at the end
+      sum[i] = fmaf(part, fast_exp2(-de), sum[i]);  // this thread's columns; the quad's are added at the end
     }
-  }
-
-  // Zeros in the place of the (scale, min) words in shared memory that are not
-  // finite, which are left to odd_values; whether there were any.  The next copy
-  // into the record comes after.
-  __device__ __noinline__ static bool drop_odd_meta(uint8_t* rec) {
-    constexpr int kWords = kBlock * (D / kGroup);
-    bool any = false;
-    for (int i = threadIdx.x % 32; i < 2 * kWords; i += 32) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(rec + i / kWords * R::kBytes + R::kVMetaOff) + i % kWords;
-      if (odd_meta(*w)) *w = 0u, any = true;
-    }
-    fence_proxy_async_shared();
-    return __any_sync(0xffffffffu, any);
   }
 
   // (scale, min) words of the thread's tokens (4 r .. of each block) and channels;
@@ -303,6 +289,19 @@ struct FewWarp {
     for (int i = 0; i < 8; ++i) {
       const float s = bf16_lo(meta[i >> 2][i & 3]), mn = bf16_hi(meta[i >> 2][i & 3]);
       top = max3_nan(top, fabsf(mn), fabsf(fmaf(s, kTop, mn)));
+    }
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  }
+
+  // Zeros in the place of words that are not finite, which are left to odd_values.
+  // Returns the bits of the largest of what remains.
+  __device__ uint32_t finite_value_meta(uint32_t (&meta)[2][4]) const {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t& w = meta[i >> 2][i & 3];
+      if (odd_meta(w)) w = 0u;
+      top = max3(top, fabsf(bf16_hi(w)), fabsf(fmaf(bf16_lo(w), kTop, bf16_hi(w))));
     }
     return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   }
@@ -486,25 +485,23 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
     }
     ok = warp_wait(bar + 8 * s, (i / kFewStages) & 1);
     if (!ok) break;
-    uint8_t* rec = smem + (warp * kFewStages + s) * L::kGroupBytes;
+    const uint8_t* rec = smem + (warp * kFewStages + s) * L::kGroupBytes;
     const int lim[2] = {(job.current ? job.stored : job.start + token[0] + 1) - t0,
                         (job.current ? job.stored : job.start + token[1] + 1) - t0};
-    float logit[4][4];
-    uint32_t value_meta[2][4], top;
+    float logit[4][4] = {};
     int ke;
-    do {  // once more where values that are not finite were dropped
-#pragma unroll
-      for (int n = 0; n < 4; ++n) logit[n][0] = logit[n][1] = logit[n][2] = logit[n][3] = 0.f;
-      if (t0 + kGroup <= job.stored) {
-        ke = w.quant_logits(rec, meta, logit);
-      } else {  // the open group's keys
-        const __nv_bfloat16* res = p.residual + (static_cast<size_t>(job.b) * p.Hkv + job.hk) * kGroup * D;
-        ke = w.exact_logits([&](int t) { return t0 + t < job.stored ? res + t * D : nullptr; }, logit);
-      }
-      top = w.quant_value_meta(rec, job.stored - t0, value_meta);
-      if (top < 0x7F800000u) break;
+    if (t0 + kGroup <= job.stored) {
+      ke = w.quant_logits(rec, meta, logit);
+    } else {  // the open group's keys
+      const __nv_bfloat16* res = p.residual + (static_cast<size_t>(job.b) * p.Hkv + job.hk) * kGroup * D;
+      ke = w.exact_logits([&](int t) { return t0 + t < job.stored ? res + t * D : nullptr; }, logit);
+    }
+    uint32_t value_meta[2][4], top = w.quant_value_meta(rec, job.stored - t0, value_meta);
+    if (top >= 0x7F800000u) {
+      asm volatile("");
       if (lane == 0) note_odd_keys(odd_at, t0, kGroup);
-    } while (w.drop_odd_meta(rec));
+      top = w.finite_value_meta(value_meta);
+    }
     const int ve = block_exp(top);
     w.weights(logit, ke, ve, lim, a);
     w.quant_output(rec, value_meta, ve, a);
@@ -523,12 +520,13 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
   }
   float* out = reinterpret_cast<float*>(smem) + warp * kFewRows * D;
   float2* stats = reinterpret_cast<float2*>(smem + L::kStats);          // [warp][16]
-  const float unit_v = pow2f(max(min(w.v_ref, 127), -149));
+  const float unit_v[2] = {pow2f(static_cast<int>(fmaxf(fminf(w.v_ref[0], 127.f), -149.f))),
+                           pow2f(static_cast<int>(fmaxf(fminf(w.v_ref[1], 127.f), -149.f)))};
 #pragma unroll
   for (int c = 0; c < W::CH; ++c)
 #pragma unroll
     for (int k = 0; k < 4; ++k)  // column 2 r + (k & 1) of channel tile c: channel CH column + c
-      out[(w.quad + 8 * (k >> 1)) * D + W::CH * (2 * w.r + (k & 1)) + c] = ok ? w.o[c][k] * unit_v : 0.f;
+      out[(w.quad + 8 * (k >> 1)) * D + W::CH * (2 * w.r + (k & 1)) + c] = ok ? w.o[c][k] * unit_v[k >> 1] : 0.f;
   if (w.r == 0) {
     stats[warp * kFewRows + w.quad] = make_float2(w.m_ref[0], w.sum[0]);
     stats[warp * kFewRows + w.quad + 8] = make_float2(w.m_ref[1], w.sum[1]);

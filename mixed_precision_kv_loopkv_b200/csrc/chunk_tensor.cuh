@@ -48,10 +48,32 @@ constexpr int kPolyPair = 3;                         // of four pairs of weights
 // codes stand two bits higher), needs no conversion.
 constexpr int kTopExp = -6;
 
-// A value block's exponent below that of the outputs counts down to 2^-60: its
-// share is nothing then, and its weights stay far above the 2^-126 that the
-// exponentials end at.
-constexpr int kLeastShift = -60;
+// The outputs of a row are held in units of 2^(m + v): m is the reference of its
+// logits (of their sum too), v an exponent that with it follows the largest
+// contribution so far, max over the blocks that the row sees of
+// 2^(largest logit) 2^(value exponent).  A weight in fp16 is then 2^(logit - m)
+// 2^(value exponent - v) <= 2^12 and precise relative to what the row adds up,
+// whatever lies in blocks that it masks or gives no weight.
+//
+// A block's exponent below v counts down to 2^-60: what it adds is nothing beside
+// the largest contribution, and the weights stay far above the 2^-126 that the
+// exponentials end at.  (Above v it has no end: its logits are as far below m.)
+constexpr float kLeastShift = -60.f;
+constexpr float kNoValueRef = -1000.f;  // v before the first
+constexpr float kLogitAbove = 8.f, kMostAbove = 12.f;  // what is not above m, v by more does not move them
+
+// Whether a row's references move: its largest new logit, and the largest of its
+// blocks' logits and value exponents together.
+__device__ __forceinline__ bool refs_move(float m, float v, float top, float most) {
+  return !(top <= m + kLogitAbove) || most > m + v + kMostAbove;
+}
+// v of a row whose reference moved from m to m_new and whose largest new
+// contribution is 2^(m_new + most).  Rounded so that 2^(m + v) of what is there
+// never grows by itself.
+__device__ __forceinline__ float value_ref(float v, float m, float m_new, float most) {
+  if (m_new != m) v = m == -INFINITY ? kNoValueRef : fmaxf(v - ceilf(m_new - m), kNoValueRef);
+  return most > v + kMostAbove ? ceilf(most) : v;
+}
 
 template <int D, int MT>
 struct ChunkSmem {
@@ -672,7 +694,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
   auto p_full = [&](int m, int buf) { return bars + 104 + 16 * m + 8 * buf; };  // its weights are there
   auto o_done = [&](int m, int buf) { return bars + 136 + 16 * m + 8 * buf; };  // and are in O
   float* k_exp = reinterpret_cast<float*>(smem + L::kKExp);
-  int* v_exp = reinterpret_cast<int*>(smem + L::kVExp);
+  float* v_exp = reinterpret_cast<float*>(smem + L::kVExp);
   OddRange* odd = reinterpret_cast<OddRange*>(smem + L::kOdd);
 
   if (threadIdx.x == 0) {
@@ -741,7 +763,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       if (j + 1 < n) loader.load(t + 1, id_next, keys);
       if (j >= 2 && !(ok = warp_wait(v_empty(s), ((j >> 1) - 1) & 1))) break;
       e = loader.store(t, id, values, sbase + L::kV + s * L::kTile);
-      if (lane == 0) v_exp[ring] = e;
+      if (lane == 0) v_exp[ring] = static_cast<float>(e);
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full(s));
@@ -848,7 +870,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       if (lane == 0) mbar_arrive(q_full);
     }
     float m_ref = -INFINITY, sum = 0.f;
-    int v_ref = -1000;
+    float v_ref = kNoValueRef;
     for (int h = 0; h < steps && ok; ++h) {
       const int j = h >> 1, buf = h & 1, gt = job.tile0 + j;
       // The tile's exponents come with its values (its keys came before).  The
@@ -875,18 +897,18 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
                        : (job.current ? job.stored : job.start + token + 1) - gt * kTileKeys) - buf * kStepKeys;
       const bool masked = __any_sync(0xffffffffu, lim < kStepKeys);
       const float4 ke = *reinterpret_cast<const float4*>(k_exp + (j % kExpRing) * kBlockWarps + buf * 4);
-      const int4 ve = *reinterpret_cast<const int4*>(v_exp + (j % kExpRing) * kBlockWarps + buf * 4);
+      const float4 ve = *reinterpret_cast<const float4*>(v_exp + (j % kExpRing) * kBlockWarps + buf * 4);
       // a scale of zero (sm_scale, or exponents out of range) must not make a number of -inf
       const float f[4] = {fmaxf(row_scale * ke.x, FLT_MIN), fmaxf(row_scale * ke.y, FLT_MIN),
                           fmaxf(row_scale * ke.z, FLT_MIN), fmaxf(row_scale * ke.w, FLT_MIN)};
-      const int vexp[4] = {ve.x, ve.y, ve.z, ve.w};
+      const float vexp[4] = {ve.x, ve.y, ve.z, ve.w};
       if (masked) {
         asm volatile("");  // a branch: most steps are not masked
 #pragma unroll
         for (int i = 0; i < kStepKeys; ++i)
           if (i >= lim) r[i] = 0xFF800000u;
       }
-      float top = -INFINITY;
+      float block_top[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint32_t* x = r + 16 * c;
@@ -897,24 +919,26 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
         a = max3_nan(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
         b = max3_nan(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
         a = max_nan(max3_nan(a, __uint_as_float(x[14]), __uint_as_float(x[15])), b);
-        top = max_nan(top, a * f[c]);
+        block_top[c] = a * f[c];
       }
-      // a NaN among the logits, or +inf, whose weight is inf - inf, is the row's
-      // reference: the weights, the sum and with them all of the row are NaN
-      top = top < INFINITY ? top : NAN;
-      const int e_top = max(max(ve.x, ve.y), max(ve.z, ve.w));
-      // The reference maximum follows the running one only when that is 2^8
-      // above it, the value exponent when a block is 2^4 above: weights stay
-      // below 2^12, and O is rescaled rarely.
-      const float m_new = top <= m_ref + 8.f ? m_ref : top;
-      const int v_new = e_top > v_ref + 4 ? e_top : v_ref;
-      if (__any_sync(0xffffffffu, m_new != m_ref) || v_new != v_ref) {
-        const float shrink = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
-        sum *= shrink;
+      float top = max_nan(max3_nan(block_top[0], block_top[1], block_top[2]), block_top[3]);
+      const float most = fmaxf(max3(block_top[0] + vexp[0], block_top[1] + vexp[1], block_top[2] + vexp[2]), block_top[3] + vexp[3]);
+      // The references follow only what is far above them: O is rescaled rarely.
+      if (__any_sync(0xffffffffu, refs_move(m_ref, v_ref, top, most))) {
+        // a NaN among the logits, or +inf, whose weight is inf - inf, is the row's
+        // reference: the weights, the sum and with them all of the row are NaN
+        top = top < INFINITY ? top : NAN;
+        const float m_new = top <= m_ref + kLogitAbove ? m_ref : top;
+        float above = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) above = fmaxf(above, block_top[c] - m_new + vexp[c]);
+        const float v_new = value_ref(v_ref, m_ref, m_new, above);
+        const float shrink = m_new == m_ref ? 0.f : m_ref - m_new;
+        sum *= fast_exp2(shrink);
         if (h > 0) {
           ok = warp_wait(o_done(m, buf ^ 1), ((h - 1) >> 1) & 1);
           tc_fence_after();
-          const float f = shrink * pow2f(max(v_ref - v_new, -149));
+          const float f = fast_exp2(shrink + (v_ref - v_new));
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             uint32_t o[16];
@@ -931,8 +955,8 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       const float base = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int de = max(vexp[c] - v_ref, kLeastShift);  // at most 4
-        const float off = static_cast<float>(de) - base;
+        const float de = fmaxf(vexp[c] - v_ref, kLeastShift);
+        const float off = de - base;
         const uint64_t f2 = pack2(f[c], f[c]), off2 = pack2(off, off);
         uint64_t part = 0;  // two sums of zero
         uint32_t w[8];
@@ -951,7 +975,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
         }
         float pa, pb;
         unpack2(part, pa, pb);
-        sum = fmaf(pa + pb, __int_as_float((127 - de) << 23), sum);
+        sum = fmaf(pa + pb, fast_exp2(-de), sum);
         tmem_st8(tp + buf * (kStepKeys / 2) + 8 * c, w);
       }
       tmem_wait_st();
@@ -971,7 +995,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     const int rows = (p.chunk.new_lens ? p.chunk.new_lens[at.b] : p.chunk.T) << p.g_log2;
     if (row - lane < rows) {
       // every row sees a key: where no logit is above -inf its weights are 0 / 0
-      const float f = pow2f(max(min(v_ref, 127), -149)) * (splits > 1 ? 1.f : m_ref == -INFINITY ? NAN : 1.f / sum);
+      const float f = pow2f(static_cast<int>(fmaxf(fminf(v_ref, 127.f), -149.f))) * (splits > 1 ? 1.f : m_ref == -INFINITY ? NAN : 1.f / sum);
       const bool valid = row < rows;
       __nv_bfloat16* o = chunk_out<D>(p, at, min(row, rows - 1));
       if (splits > 1) reinterpret_cast<float2*>(smem + L::kStats)[local] = make_float2(m_ref, sum);

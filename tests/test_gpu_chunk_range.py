@@ -1,0 +1,108 @@
+"""Chunk attention over numbers of far-apart and of extreme sizes: a row's
+precision follows what it sees and weighs."""
+
+import numpy as np
+import pytest
+import torch
+
+from loopkv_testlib import seeded_bf16
+from oracle import chunk_oracle as CO
+from test_gpu_chunk import cell_for, host, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixed_precision_kv_loopkv_b200 as pkg
+    return pkg
+
+
+def block_tops(vh, n, size):
+    """The largest absolute value of each token's block of `size` tokens, over the n
+    stored tokens and, counted anew, over the current ones."""
+    top = np.zeros(vh.shape[0])
+    for lo, hi in ((0, n), (n, vh.shape[0])):
+        for t in range(lo, hi, size):
+            top[t: min(t + size, hi)] = np.abs(vh[t: min(t + size, hi)]).max()
+    return top
+
+
+def attend_seen(q, kh, vh, last, sm, n, size, quantised):
+    """chunk_attend's rows with a slack that counts only what a row sees and weighs.
+
+    With t_j the largest value of key j's block (size: 16, few rows 32) and u = 2^-11:
+    weights as there; a value entry is off by 4 u t_j at most where it is a rounded
+    minimum (t_j) plus a rounded scale times a code (2 t_j), rounded (t_j), and by
+    2^-18 t_j where it is exact (half a subnormal step, 2^-25, beside a largest entry
+    of 2^-7 or more); a weight below 2^-14 of the outputs' scale 2^R is off by 2^-25
+    of that.  2^R is at most twice max_j p_j 2^(e_j), and the block's power of two
+    2^(e_j) puts its largest entry into [2^(c-1), 2^c) for one c, all entries below
+    2^c: 2^-25 x 2 x 2 max_j(p_j t_j) = 2^-23 max_j(p_j t_j) for each key.
+    """
+    top = block_tops(vh, n, size)
+    want, slack = np.zeros(q.shape), np.zeros(q.shape)
+    u = 2.0**-11
+    entry = 4 * u if quantised else 2.0**-18
+    for i in range(q.shape[0]):
+        k, v, t = kh[: last[i] + 1], vh[: last[i] + 1], top[: last[i] + 1]
+        s = sm * (k @ q[i])
+        e = np.exp(s - s.max())
+        p = e / e.sum()
+        want[i] = p @ v
+        dj = (u + q.shape[1] * 2.0**-23) * abs(sm) * (np.abs(k) @ np.abs(q[i]))
+        w = p * (dj + p @ dj + u + 2.0**-16)
+        slack[i] = 1.05 * (w @ np.abs(v) + entry * (p @ t) + len(p) * 2.0**-23 * (p * t).max()) + 2.0**-8 * np.abs(want[i])
+    return want, slack
+
+
+def far_case(m, kind, d, T, start, current, change, seed=0, sm=0.5, B=1, heads=2, rows=None):
+    n = start if current else start + T
+    k, v = (seeded_bf16((B, start + T, 1, d), seed + i) for i in range(2))
+    q = seeded_bf16((B, T, heads, d), seed + 2, 0.3)
+    change(q, k, v)
+    kv, table = cell_for(m, kind, B, 1, d, max(n, 1), heads, seed)
+    m.loopkv_rope_append(kv, 0, 0, None, None, k[:, :n], v[:, :n], table, ints([0] * B))
+    cur = dict(k_cur=k[:, n:], v_cur=v[:, n:]) if current else {}
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([start] * B), sm_scale=sm, **cur)
+    rows = np.arange(T) if rows is None else np.asarray(rows)
+    quantised = kind != "bf16"
+    size = 32 if quantised and T * heads <= 16 else 16
+    for b in range(B):
+        kh, vh = CO.stored_values(kind, host(k[b, :n, 0]), host(v[b, :n, 0]))
+        kh, vh = np.vstack([kh, host(k[b, n:, 0])]).astype(np.float64), np.vstack([vh, host(v[b, n:, 0])]).astype(np.float64)
+        for h in range(heads):
+            want, slack = attend_seen(host(q[b, rows, h]).astype(np.float64), kh, vh, start + rows, sm, n, size, quantised)
+            off = np.abs(host(out[b, rows, h]) - want)
+            assert np.all(off <= slack), (b, h, float((off / slack).max()), int((off / slack).max(1).argmax()))
+
+
+@pytest.mark.parametrize("kind,current", [("q4", False), ("q2", False), ("bf16", False), ("q4", True), ("bf16", True)])
+@pytest.mark.parametrize("big", [2.0**14, 2.0**20, 2.0**26, 2.0**40, 2.0**90])
+@pytest.mark.parametrize("T,start,first", [(150, 0, 16), (150, 0, 64), (140, 0, 128), (8, 28, 32), (300, 20, 160)])
+def test_values_that_a_row_does_not_see(m, kind, current, big, T, start, first):
+    """Later tokens' values are far larger than those that the early rows see."""
+    if current and T < 100:
+        pytest.skip("the chunk's few rows are one block")
+    at = start + (first - start + 15) // 16 * 16 if current else first     # where a block begins
+
+    def change(q, k, v):
+        v[:, at:] *= big
+
+    far_case(m, kind, 64, T, start, current, change)
+
+
+@pytest.mark.parametrize("kind,current", [("q4", False), ("q2", False), ("bf16", False), ("q4", True)])
+@pytest.mark.parametrize("big,down", [(2.0**16, 30), (2.0**24, 40), (2.0**40, 70), (2.0**60, 80), (2.0**40, 20), (2.0**100, 150)])
+@pytest.mark.parametrize("T,start", [(7, 500), (150, 500), (150, 1900)])
+def test_large_values_of_little_weight(m, kind, current, big, down, T, start):
+    """Some groups have values far larger, and logits far smaller (by 2^-down of the
+    weight): what they add is as little or as much as it is."""
+    def change(q, k, v):
+        k[..., 0] = 0
+        q[..., 0] = 1.0
+        for lo in (0, 96, 288):
+            k[:, lo: lo + 32, :, 0] = -2 * down * np.log(2.0)      # sm = 0.5
+            v[:, lo: lo + 32] *= big
+        k[:, 416: 448, :, 0] = 20.0                                 # late in the context the maximum moves up
+    far_case(m, kind, 64, T, start, current, change, seed=4, rows=range(0, T, max(1, T // 12)))
