@@ -39,11 +39,11 @@ struct FewSmem {
   static constexpr int kRing = WARPS * kFewStages * kGroupBytes;
   static constexpr int kOut = WARPS * kFewRows * D * 4;          // the warps' partial outputs, over the ring
   static constexpr int kMeta = (kRing > kOut ? kRing : kOut);        // each warp: a group's key scales and minima
-  static constexpr int kStats = kMeta + WARPS * D * 4;           // each warp: (max, sum) of 16 rows
-  static constexpr int kOdd = kStats + WARPS * kFewRows * 8;     // each warp: OddRange
+  static constexpr int kStats = kMeta + WARPS * D * 4;           // each warp: RowStats of 16 rows
+  static constexpr int kOdd = kStats + WARPS * kFewRows * 16;    // each warp: OddRange
   static constexpr int kJoin = kOdd + WARPS * 16;
   static constexpr int kJoinStats = kJoin + kFewRows * D * 4;        // the CTA's own result, for its cluster
-  static constexpr int kBars = kJoinStats + kFewRows * 8;
+  static constexpr int kBars = kJoinStats + kFewRows * 16;
   static constexpr int kBytes = kBars + WARPS * kFewStages * 8;
 };
 
@@ -519,17 +519,15 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
     w.sum[i] += __shfl_xor_sync(0xffffffffu, w.sum[i], 2);
   }
   float* out = reinterpret_cast<float*>(smem) + warp * kFewRows * D;
-  float2* stats = reinterpret_cast<float2*>(smem + L::kStats);          // [warp][16]
-  const float unit_v[2] = {pow2f(static_cast<int>(fmaxf(fminf(w.v_ref[0], 127.f), -149.f))),
-                           pow2f(static_cast<int>(fmaxf(fminf(w.v_ref[1], 127.f), -149.f)))};
+  RowStats* stats = reinterpret_cast<RowStats*>(smem + L::kStats);      // [warp][16]
 #pragma unroll
   for (int c = 0; c < W::CH; ++c)
 #pragma unroll
     for (int k = 0; k < 4; ++k)  // column 2 r + (k & 1) of channel tile c: channel CH column + c
-      out[(w.quad + 8 * (k >> 1)) * D + W::CH * (2 * w.r + (k & 1)) + c] = ok ? w.o[c][k] * unit_v[k >> 1] : 0.f;
+      out[(w.quad + 8 * (k >> 1)) * D + W::CH * (2 * w.r + (k & 1)) + c] = ok ? w.o[c][k] : 0.f;
   if (w.r == 0) {
-    stats[warp * kFewRows + w.quad] = make_float2(w.m_ref[0], w.sum[0]);
-    stats[warp * kFewRows + w.quad + 8] = make_float2(w.m_ref[1], w.sum[1]);
+    stats[warp * kFewRows + w.quad] = RowStats{w.m_ref[0], w.sum[0], w.v_ref[0]};
+    stats[warp * kFewRows + w.quad + 8] = RowStats{w.m_ref[1], w.sum[1], w.v_ref[1]};
   }
   // what follows is worked out anew, so as not to hold it over the groups
   ChunkJob at;
@@ -550,27 +548,22 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
   __syncthreads();
   constexpr int kQuads = D / 4;
   float4* join = reinterpret_cast<float4*>(smem + L::kJoin);
-  float2* join_stats = reinterpret_cast<float2*>(smem + L::kJoinStats);
+  RowStats* join_stats = reinterpret_cast<RowStats*>(smem + L::kJoinStats);
   for (int i = threadIdx.x; i < rows * kQuads; i += kThreads) {
     const int row = i / kQuads, col = i % kQuads;
-    float m = -INFINITY, sum = 0.f;
-    for (int k = 0; k < WARPS; ++k) m = fmaxf(m, stats[k * kFewRows + row].x);
+    auto stats_of = [&](int k) { return stats[k * kFewRows + row]; };
+    RowStats all = join_refs(WARPS, stats_of);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < WARPS; ++k) {
-      const float2 st = stats[k * kFewRows + row];
-      if (st.x == -INFINITY) continue;  // it saw no key, or none with a weight
-      const float g = fast_exp2(st.x - m);
-      const float4 x = reinterpret_cast<const float4*>(smem)[(k * kFewRows + row) * kQuads + col];
-      sum = fmaf(g, st.y, sum);
-      acc.x = fmaf(g, x.x, acc.x), acc.y = fmaf(g, x.y, acc.y), acc.z = fmaf(g, x.z, acc.z), acc.w = fmaf(g, x.w, acc.w);
+      const RowStats st = stats_of(k);
+      if (st.m == -INFINITY) continue;
+      join_part(all, st, acc, reinterpret_cast<const float4*>(smem)[(k * kFewRows + row) * kQuads + col]);
     }
     if (splits == 1) {
-      const float inv = 1.f / sum;  // 0 / 0 where no logit is above -inf
-      reinterpret_cast<uint2*>(chunk_out<D>(p, at, row))[col] =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      reinterpret_cast<uint2*>(chunk_out<D>(p, at, row))[col] = join_result(all, acc);
     } else {
       join[i] = acc;
-      if (col == 0) join_stats[row] = make_float2(m, sum);
+      if (col == 0) join_stats[row] = all;
     }
   }
   if (splits == 1) return;
@@ -579,7 +572,7 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
   for (int i = threadIdx.x; i < rows * kQuads; i += kThreads) {
     if (i / 32 % splits != rank_again) continue;
     const int row = i / kQuads;
-    join_splits<D>(p, at, row, i % kQuads, splits, sbase + L::kJoinStats + row * 8, sbase + L::kJoin + i * 16);
+    join_splits<D>(p, at, row, i % kQuads, splits, sbase + L::kJoinStats + row * 16, sbase + L::kJoin + i * 16);
   }
   cluster_sync_all();
 }

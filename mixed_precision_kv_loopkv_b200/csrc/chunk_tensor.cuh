@@ -75,6 +75,37 @@ __device__ __forceinline__ float value_ref(float v, float m, float m_new, float 
   return most > v + kMostAbove ? ceilf(most) : v;
 }
 
+// A partial result of a row: its outputs are in units of 2^(m + v), its sum of 2^m.
+struct alignas(16) RowStats {
+  float m, sum, v;
+};
+
+// The references of several partial results together: m is their largest, m + v the
+// largest unit.  `next` gives them one after another.
+template <typename Next>
+__device__ __forceinline__ RowStats join_refs(int count, Next&& next) {
+  float m = -INFINITY, unit = -INFINITY;
+  for (int i = 0; i < count; ++i) {
+    const RowStats s = next(i);
+    m = fmaxf(m, s.m);
+    unit = fmaxf(unit, s.m + s.v);
+  }
+  return RowStats{m, 0.f, unit - m};
+}
+// One of them into sum and outputs; skipped where it saw no key, or none with a weight.
+__device__ __forceinline__ void join_part(RowStats& all, const RowStats& s, float4& acc, const float4& x) {
+  const float d = s.m - all.m, w = fast_exp2(d + s.v - all.v);
+  all.sum = fmaf(fast_exp2(d), s.sum, all.sum);
+  acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
+}
+// Outputs over sum, times their unit, in two steps: v may be beyond 127, and the
+// average be finite where its sum is not.  0 / 0 where no logit is above -inf.
+__device__ __forceinline__ uint2 join_result(const RowStats& all, const float4& acc) {
+  const float inv = 1.f / all.sum, unit = fast_exp2(all.v * 0.5f);
+  return make_uint2(pack_bf16(acc.x * inv * unit * unit, acc.y * inv * unit * unit),
+                    pack_bf16(acc.z * inv * unit * unit, acc.w * inv * unit * unit));
+}
+
 template <int D, int MT>
 struct ChunkSmem {
   static constexpr int kTile = kTileKeys * D * 2;    // one K or V stage, one Q tile
@@ -84,8 +115,8 @@ struct ChunkSmem {
   static constexpr int kMeta = kV + 2 * kTile;       // per key warp: its group's scales and minima, fp16
   static constexpr int kKExp = kMeta + kBlockWarps * D * 4;            // 16-byte aligned
   static constexpr int kVExp = kKExp + kExpRing * kBlockWarps * 4;
-  static constexpr int kStats = kVExp + kExpRing * kBlockWarps * 4;     // (max, sum) of each row
-  static constexpr int kBars = kStats + MT * 128 * 8;
+  static constexpr int kStats = kVExp + kExpRing * kBlockWarps * 4;     // RowStats
+  static constexpr int kBars = kStats + MT * 128 * 16;
   static constexpr int kBarCount = 9 + 2 * 6;
   static constexpr int kTmem = kBars + kBarCount * 8;
   static constexpr int kOdd = kTmem + 8;             // OddRange
@@ -345,34 +376,29 @@ __device__ bool chunk_job(const ChunkAttnParams& p, ChunkJob& job, int row0, int
   return false;
 }
 
-// Four channels of a row out of its splits' partial results: (max, sum) at
-// `stats` and channels at `part` in the shared memory of each CTA of the cluster.
+// Four channels of a row out of its splits' partial results: RowStats at `stats`
+// and channels at `part` in the shared memory of each CTA of the cluster.
 template <int D>
 __device__ __forceinline__ void join_splits(const ChunkAttnParams& p, const ChunkJob& job, int row, int quad, int splits,
                                             uint32_t stats, uint32_t part) {
-  float top = -INFINITY;
-  for (int s = 0; s < splits; ++s) {
-    float m;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m) : "r"(peer_addr(stats, s)) : "memory");
-    top = fmaxf(top, m);
-  }
-  float sum = 0.f;
+  auto stats_of = [&](int s) {
+    RowStats r;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(r.m), "=f"(r.sum) : "r"(peer_addr(stats, s)) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r.v) : "r"(peer_addr(stats + 8, s)) : "memory");
+    return r;
+  };
+  RowStats all = join_refs(splits, stats_of);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = 0; s < splits; ++s) {
-    float m, l;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(peer_addr(stats, s)) : "memory");
-    if (m == -INFINITY) continue;  // it saw no key, or none with a weight
-    const float w = fast_exp2(m - top);
+    const RowStats st = stats_of(s);
+    if (st.m == -INFINITY) continue;
     float4 x;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
                  : "r"(peer_addr(part, s)) : "memory");
-    sum = fmaf(w, l, sum);
-    acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
+    join_part(all, st, acc, x);
   }
-  const float inv = 1.f / sum;  // 0 / 0 where no split had a logit above -inf
-  reinterpret_cast<uint2*>(chunk_out<D>(p, job, row))[quad] =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  reinterpret_cast<uint2*>(chunk_out<D>(p, job, row))[quad] = join_result(all, acc);
 }
 
 // ---------------------------------------------------------------- dequantising warps
@@ -994,11 +1020,15 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     at.b = unit_again / row_tiles / p.Hkv;
     const int rows = (p.chunk.new_lens ? p.chunk.new_lens[at.b] : p.chunk.T) << p.g_log2;
     if (row - lane < rows) {
-      // every row sees a key: where no logit is above -inf its weights are 0 / 0
-      const float f = pow2f(static_cast<int>(fmaxf(fminf(v_ref, 127.f), -149.f))) * (splits > 1 ? 1.f : m_ref == -INFINITY ? NAN : 1.f / sum);
+      // Over the sum, times the unit, in two steps (v may be beyond 127); partial
+      // results go as they are.  Every row sees a key: where no logit is above -inf
+      // its weights are 0 / 0.
+      const float near = fmaxf(fminf(v_ref, 100.f), -100.f);
+      const float f1 = splits > 1 ? 1.f : m_ref == -INFINITY ? NAN : pow2f(static_cast<int>(near)) / sum;
+      const float f2 = splits > 1 ? 1.f : pow2f(static_cast<int>(fmaxf(v_ref - near, -49.f)));
       const bool valid = row < rows;
       __nv_bfloat16* o = chunk_out<D>(p, at, min(row, rows - 1));
-      if (splits > 1) reinterpret_cast<float2*>(smem + L::kStats)[local] = make_float2(m_ref, sum);
+      if (splits > 1) reinterpret_cast<RowStats*>(smem + L::kStats)[local] = RowStats{m_ref, sum, v_ref};
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t r[32];
@@ -1011,7 +1041,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
         }
         float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = ok ? __uint_as_float(r[i]) * f : 0.f;
+        for (int i = 0; i < 32; ++i) x[i] = ok ? __uint_as_float(r[i]) * f1 * f2 : 0.f;
         if (splits == 1) {
           if (valid) {
 #pragma unroll
@@ -1049,8 +1079,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
   if (splits == 1) return;
 
   // ---------------------------------------------------------------- join the splits
-  // Every CTA holds its partial rows (times their value exponent) and their
-  // (max, sum); row i is put together by CTA i % splits from all of them.
+  // Every CTA holds its partial rows and their RowStats; row i is put together by CTA i % splits from all of them.
   cluster_sync_all();
   {
     const uint32_t stats = sbase + L::kStats, partial = sbase + L::kPartial;
@@ -1066,7 +1095,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     for (int i = warp * kRowsPerWarp + lane / kQuads;; i += kSoftmaxWarps * kRowsPerWarp) {
       const int row = i * splits + rank;
       if (row >= rows) break;
-      join_splits<D>(p, at, first + row, quad, splits, stats + row * 8,
+      join_splits<D>(p, at, first + row, quad, splits, stats + row * 16,
                      partial + row * D * 4 + ((quad ^ (row & (kQuads - 1))) << 4));
     }
   }

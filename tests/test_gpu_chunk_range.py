@@ -106,3 +106,14 @@ def test_large_values_of_little_weight(m, kind, current, big, down, T, start):
             v[:, lo: lo + 32] *= big
         k[:, 416: 448, :, 0] = 20.0                                 # late in the context the maximum moves up
     far_case(m, kind, 64, T, start, current, change, seed=4, rows=range(0, T, max(1, T // 12)))
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2", "bf16"])
+@pytest.mark.parametrize("current", [False, True])
+@pytest.mark.parametrize("T,start", [(5, 1500), (5, 40), (140, 1500), (300, 40)])
+@pytest.mark.parametrize("v_scale", [2.0**118, 2.0**125, 2.0**-110])
+def test_values_at_the_ends_of_the_range(m, kind, current, T, start, v_scale):
+    """Averages of values near the largest number, and of very small ones."""
+    def change(q, k, v):
+        v.copy_((v.float().clamp(-3, 3).abs() if v_scale > 2.0**120 else v.float()).mul(v_scale).bfloat16())
+    far_case(m, kind, 64, T, start, current, change, seed=8, rows=range(0, T, max(1, T // 9)))
