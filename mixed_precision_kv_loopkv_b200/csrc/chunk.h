@@ -72,7 +72,8 @@ struct ChunkAttnParams {
   ChunkView chunk;
   int H, Hkv, g_log2, max_blocks, num_blocks;
   int max_stored;                // host bound of the stored tokens
-  float sm_scale_log2;           // sm_scale * log2(e)
+  float scale_mantissa;          // |sm_scale * log2(e)| = mantissa in [1, 2) times 2^exp
+  int scale_exp, scale_negative;
 };
 
 cudaError_t launch_norm_rope(int head_dim, const RotateParams& p, cudaStream_t stream);

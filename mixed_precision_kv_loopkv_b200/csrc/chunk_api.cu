@@ -213,7 +213,12 @@ loopkv_status loopkv_chunk_attention(const loopkv_config* cfg, const loopkv_cell
   p.g_log2 = group == 8 ? 3 : group == 4 ? 2 : group == 2 ? 1 : 0;
   p.max_blocks = cfg->max_blocks_per_seq;
   p.num_blocks = cfg->num_blocks;
-  p.sm_scale_log2 = sm_scale * kLog2e;
+  const double scale = fabs(sm_scale * 1.4426950408889634);
+  p.scale_mantissa = static_cast<float>(2.0 * frexp(scale, &p.scale_exp));
+  p.scale_exp -= 1;
+  if (scale == 0.0) p.scale_mantissa = 1.f, p.scale_exp = -10000;  // far below anything
+  if (p.scale_mantissa == 2.f) p.scale_mantissa = 1.f, p.scale_exp += 1;  // rounded up
+  p.scale_negative = sm_scale < 0.f;
   return result(launch_chunk_attention(cfg->plan[cell], cfg->head_dim, p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -73,7 +73,7 @@ struct FewWarp {
   const ChunkJob& job;
   int lane, quad, r;
   uint32_t q[STEPS][4];
-  float row_scale[2];          // rows quad, quad + 8
+  int row_exp[2];              // rows quad, quad + 8: of the queries, and the scale's
   float m_ref[2], sum[2];
   float v_ref[2];
   float o[CH][4];
@@ -87,9 +87,8 @@ struct FewWarp {
     for (int i = 0; i < CH; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
 
-  // Rows quad and quad + 8, this thread's D / 4 channels, in [2^13, 2^14).
+  // Rows quad and quad + 8, this thread's D / 4 channels.
   __device__ void load_queries(int rows) {
-    const float sign = p.sm_scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = quad + 8 * i;
@@ -109,9 +108,9 @@ struct FewWarp {
       top = max(top & 0xFFFFu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = max(static_cast<int>(top >> 7) - 127 - 13, -100);
-      const float f = sign * pow2f(-e);
-      row_scale[i] = fabsf(p.sm_scale_log2) * pow2f(e);
+      const int e = query_exp(top);
+      const float f = p.scale_negative ? -pow2f(-e) : pow2f(-e);
+      row_exp[i] = e + p.scale_exp;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {  // eight channels: two steps
         q[2 * k][i] = bf16x2_to_half(w[k].x, f), q[2 * k][2 + i] = bf16x2_to_half(w[k].y, f);
@@ -198,7 +197,7 @@ struct FewWarp {
           top = abs_max_bf16x8(top, finite_bf16x8(reinterpret_cast<const uint4*>(src + r * (D / 4))[k]));
         }
     }
-    const int e = block_exp<kExactTopExp>(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
+    const int e = block_exp<kExactTopExp, kLeastExp>(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
     const float f = pow2f(-e);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
@@ -217,7 +216,6 @@ struct FewWarp {
   // Logits to weights, in place: 2^(logit - m_ref) 2^(ve - v_ref) as fp16 pairs a[block][4], the
   // products' left operand.  lim[i]: keys of the group that row quad + 8 i sees.
   __device__ void weights(float (&s)[4][4], int ke, int ve, const int (&lim)[2], uint32_t (&a)[2][4]) {
-    const float k = block_scale(ke);
     bool masked = __any_sync(0xffffffffu, lim[0] < kGroup || lim[1] < kGroup);
     if (masked) {
       asm volatile("");
@@ -232,7 +230,7 @@ struct FewWarp {
     bool move = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f[i] = fmaxf(row_scale[i] * k, FLT_MIN);  // not zero, for -inf's sake
+      f[i] = logit_scale(p.scale_mantissa, row_exp[i] + ke);
       float t = max_nan(max3_nan(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), max3_nan(s[1][2 * i + 1], s[2][2 * i], s[2][2 * i + 1]));
       t = max3_nan(t, s[3][2 * i], s[3][2 * i + 1]) * f[i];
       t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, 1));
@@ -373,7 +371,7 @@ struct FewWarp {
         }
     }
     odd = __any_sync(0xffffffffu, some);
-    return block_exp(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
+    return block_exp<kTopExp, kLeastExp>(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) << 16);
   }
 
   template <typename Row>

@@ -28,7 +28,6 @@
 #pragma once
 
 #include <cuda_fp16.h>
-#include <float.h>
 
 #include "chunk_common.cuh"
 #include "tcgen05.cuh"
@@ -151,14 +150,14 @@ __device__ __forceinline__ float pow2f(int e) {
 
 // Exponent e of a block whose largest absolute value has the float bits u:
 // the value times 2^-e is in [2^(TOP - 1), 2^TOP) (smaller where e is held at
-// -100).  Exact rows have no codes to make room for: their keys, and a bf16
+// -100, or -127 for exact rows).  Exact rows have no codes to make room for: their keys, and a bf16
 // cell's values, stand at 2^8, which leaves entries 2^-22 of the largest whole.
 // Exact values beside quantised ones keep to the place of those, since one
 // exponent serves the outputs of both.
-constexpr int kExactTopExp = 8;
-template <int TOP = kTopExp>
+constexpr int kExactTopExp = 8, kLeastExp = -127;
+template <int TOP = kTopExp, int LEAST = -100>
 __device__ __forceinline__ int block_exp(uint32_t abs_bits) {
-  return max(static_cast<int>(abs_bits >> 23) - 127 - TOP + 1, -100);
+  return max(static_cast<int>(abs_bits >> 23) - 127 - TOP + 1, LEAST);
 }
 
 // The upper two bits of each nibble from hi, the lower two from lo: one
@@ -175,8 +174,19 @@ __device__ __forceinline__ float block_unit(int e) {
   static_assert(K >= 20 && K <= 24, "e is in [-100, 134]");
   return __int_as_float((127 + K - e) << 23);
 }
-// 2^e, at most 2^127 (keys beyond 2^120 have no finite logits anyway).
-__device__ __forceinline__ float block_scale(int e) { return __int_as_float((min(e, 127) + 127) << 23); }
+
+// Exponent of a query row whose largest absolute value has the bf16 bits u: the
+// row times 2^-e has it in [2^13, 2^14) (bf16's 8 bits stay whole in fp16).
+__device__ __forceinline__ int query_exp(uint32_t abs_bits) {
+  return max(static_cast<int>(abs_bits >> 7) - 127 - 13, kLeastExp);
+}
+// What turns a product into a logit: the scale's mantissa times 2^e, e the sum of
+// the scale's, the row's and the keys' exponents, each of which may be far out.
+// At least 2^-126 (a scale of zero must not make a number of -inf), at most a
+// finite number (nor one of a product of zero).
+__device__ __forceinline__ float logit_scale(float mantissa, int e) {
+  return __int_as_float(__float_as_int(mantissa) + (min(max(e, -126), 127) << 23));
+}
 
 // 16 channels' codes (hi << 2 | lo, two bits each plane; 2-bit cells: code << 2)
 // as fp16 x = code s + m: eight half2 words of neighbouring channels.  s, m:
@@ -545,7 +555,7 @@ struct BlockLoader {
       top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
       if (!KEYS && lane == 0) note_odd_keys(odd_at, token0(tile), kBlock);
     }
-    const int e = block_exp<KEYS || !kQuant ? kExactTopExp : kTopExp>(top << 16);
+    const int e = block_exp<KEYS || !kQuant ? kExactTopExp : kTopExp, kLeastExp>(top << 16);
     const float f = pow2f(-e);
 #pragma unroll
     for (int k = 0; k < KPL; ++k) {
@@ -719,7 +729,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
   auto s_free = [&](int m) { return bars + 88 + 8 * m; };                       // and have been read
   auto p_full = [&](int m, int buf) { return bars + 104 + 16 * m + 8 * buf; };  // its weights are there
   auto o_done = [&](int m, int buf) { return bars + 136 + 16 * m + 8 * buf; };  // and are in O
-  float* k_exp = reinterpret_cast<float*>(smem + L::kKExp);
+  int* k_exp = reinterpret_cast<int*>(smem + L::kKExp);
   float* v_exp = reinterpret_cast<float*>(smem + L::kVExp);
   OddRange* odd = reinterpret_cast<OddRange*>(smem + L::kOdd);
 
@@ -782,7 +792,7 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       const int2 id_after = j + 2 < n ? loader.ids(t + 2) : id_next;
       if (j >= 2 && !(ok = warp_wait(k_empty(s), ((j >> 1) - 1) & 1))) break;
       int e = loader.store(t, id, keys, sbase + L::kK + s * L::kTile, sbase + L::kMeta + block * D * 4);
-      if (lane == 0) k_exp[ring] = block_scale(e);
+      if (lane == 0) k_exp[ring] = e;
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full(s));
@@ -862,9 +872,8 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
     const uint32_t ts = tmem + m * kStepKeys + lanes, tp = tmem_p + m * kStepKeys + lanes, to = tmem_o + m * D + lanes;
     const bool idle = row0 + warp * 32 >= row_end;                 // no row of this warp is there
     const int token = my_row >> p.g_log2;
-    // Queries: a row a thread, times a power of two that brings its largest entry
-    // to [2^13, 2^14) (bf16's 8 bits stay whole in fp16), the scale's sign with it.
-    float row_scale;
+    // Queries: a row a thread, times a power of two, the scale's sign with it.
+    int row_exp;
     {
       const uint4* src = reinterpret_cast<const uint4*>(row_at(p.q, job.b, token, (job.hk << p.g_log2) + (my_row & ((1 << p.g_log2) - 1))));
       uint32_t top = 0;
@@ -877,9 +886,9 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
         for (int i = 0; i < D / 16; ++i)
           top = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(top, w[i].x), w[i].y), w[i].z), w[i].w);
       }
-      const int e = max(static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127 - 13, -100);
-      const float f = p.sm_scale_log2 < 0.f ? -pow2f(-e) : pow2f(-e);
-      row_scale = fabsf(p.sm_scale_log2) * pow2f(e);
+      const int e = query_exp(max(top & 0xFFFFu, top >> 16));
+      const float f = p.scale_negative ? -pow2f(-e) : pow2f(-e);
+      row_exp = e + p.scale_exp;
       const uint32_t q = sbase + L::kQ + m * L::kTile;
 #pragma unroll
       for (int half = 1; half >= 0; --half) {  // the second half is still here
@@ -922,11 +931,10 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       const int lim = (gt >= job.stored_tiles ? token + 1 - (gt - job.stored_tiles) * kTileKeys
                        : (job.current ? job.stored : job.start + token + 1) - gt * kTileKeys) - buf * kStepKeys;
       const bool masked = __any_sync(0xffffffffu, lim < kStepKeys);
-      const float4 ke = *reinterpret_cast<const float4*>(k_exp + (j % kExpRing) * kBlockWarps + buf * 4);
+      const int4 ke = *reinterpret_cast<const int4*>(k_exp + (j % kExpRing) * kBlockWarps + buf * 4);
       const float4 ve = *reinterpret_cast<const float4*>(v_exp + (j % kExpRing) * kBlockWarps + buf * 4);
-      // a scale of zero (sm_scale, or exponents out of range) must not make a number of -inf
-      const float f[4] = {fmaxf(row_scale * ke.x, FLT_MIN), fmaxf(row_scale * ke.y, FLT_MIN),
-                          fmaxf(row_scale * ke.z, FLT_MIN), fmaxf(row_scale * ke.w, FLT_MIN)};
+      const float f[4] = {logit_scale(p.scale_mantissa, row_exp + ke.x), logit_scale(p.scale_mantissa, row_exp + ke.y),
+                          logit_scale(p.scale_mantissa, row_exp + ke.z), logit_scale(p.scale_mantissa, row_exp + ke.w)};
       const float vexp[4] = {ve.x, ve.y, ve.z, ve.w};
       if (masked) {
         asm volatile("");  // a branch: most steps are not masked

@@ -117,3 +117,16 @@ def test_values_at_the_ends_of_the_range(m, kind, current, T, start, v_scale):
     def change(q, k, v):
         v.copy_((v.float().clamp(-3, 3).abs() if v_scale > 2.0**120 else v.float()).mul(v_scale).bfloat16())
     far_case(m, kind, 64, T, start, current, change, seed=8, rows=range(0, T, max(1, T // 9)))
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2", "bf16"])
+@pytest.mark.parametrize("current", [False, True])
+@pytest.mark.parametrize("T,start", [(5, 100), (140, 100)])
+@pytest.mark.parametrize("k_pow,q_pow,s_pow", [(121, 0, -121), (121, -121, 0), (121, -60, -61), (-90, 100, -10), (-90, 0, 90),
+                                               (90, 36, -126), (-60, -60, 120), (60, -100, 40)])
+def test_keys_queries_and_scale_far_from_one(m, kind, current, T, start, k_pow, q_pow, s_pow):
+    """Logits of ordinary size out of keys, queries and a scale that are not."""
+    def change(q, k, v):
+        k.mul_(2.0**k_pow)
+        q.mul_(2.0**q_pow)
+    far_case(m, kind, 64, T, start, current, change, seed=12, sm=0.5 * 2.0**s_pow, rows=range(0, T, max(1, T // 9)))
