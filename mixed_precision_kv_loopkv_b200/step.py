@@ -24,11 +24,18 @@ final loop's tokens of the earlier chunks and the chunk's own exact rows.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from .chunk import Rotary, loopkv_chunk_attention, loopkv_norm_rope, loopkv_rope_append
 from .loopkv import (LOOPKV_CELL_REUSE, KVCells, loopkv_append_decode_attention, loopkv_decode_attention,
                      loopkv_quantize_append)
+
+
+def _on(stream):
+    """Torch operations on the stream, or on the current one for None."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def prefill(kv: KVCells, loop: int, layer: int, k, v, block_table, lens, err_flag=None, stream=None):
@@ -131,7 +138,9 @@ class LoopedChunkStep:
     """A chunk of new tokens through every (loop, layer) cell, in order.
 
     Two launches a cell: loopkv_rope_append (reuse cells: loopkv_norm_rope) and
-    loopkv_chunk_attention.
+    loopkv_chunk_attention.  A sequence whose chunk does not fit the block table
+    or a layer's rotation table, or whose length is outside [0, T], is flagged,
+    and none of its cells stores or answers anything (its rows are zeros).
 
     start   : device int32[B], stored tokens of every sequence (negative: the
               sequence is skipped); ``advance()`` moves it by the chunk
@@ -151,35 +160,60 @@ class LoopedChunkStep:
             raise ValueError("one rotary for all layers or one for each")
         self.sm_scale, self.max_seq_len, self.err_flag = sm_scale, max_seq_len, err_flag
         self.cells = list(range(len(kv.plan_codes))) if cells is None else sorted(cells)
-        # rotated queries (and a reuse cell's keys): one cell's at a time; what a
-        # chunk does not write there it does not read
+        # rotated queries (and a reuse cell's keys): one cell's at a time
         shapes = {"q": self.q[self.cells[0]].shape, "k": self.k[self.cells[0]].shape} if self.cells else {}
         self._rows = {name: torch.empty(shape, dtype=torch.bfloat16, device=start.device) for name, shape in shapes.items()}
+        self._tokens = shapes["q"][1] if shapes else 0
+        capacity = kv.max_blocks_per_seq * kv.block_size
+        tables = [self.rotary[c % kv.num_layers].table for c in self.cells]
+        positions = min((t.shape[0] for t in tables if t is not None), default=capacity + self._tokens)
+        self._limit = min(capacity, positions)
+        # Norms and appends skip a sequence that runs past its rotation table, which
+        # the attention does not know of: it would read rows that were never
+        # written.  Where a table does not reach as far as the attention answers
+        # (a reuse cell: the chunk behind a full cell), both are told beforehand.
+        reuse = any(kv.plan_codes[c] == LOOPKV_CELL_REUSE for c in self.cells)
+        self._guard = positions < capacity + (self._tokens if reuse else 0)
 
     def launches_per_step(self) -> int:
         return 2 * len(self.cells)
+
+    def _fits(self):
+        """Device bool[B]: whether the sequence's chunk is one (its start may be negative)."""
+        if self.lens is None:
+            return self.start <= self._limit - self._tokens
+        n = self.lens
+        return (n == 0) | ((n > 0) & (n <= self._tokens) & (self.start <= self._limit - n))
 
     def run(self, stream=None):
         """Enqueue the chunk.  Not to be run twice at the same place without
         ``advance()``: storing a chunk completes key groups whose exact keys the
         chunk's own last tokens then replace."""
         kv, qr = self.kv, self._rows.get("q")
+        lens, start = self.lens, self.start
+        if self._guard and self.cells:
+            with _on(stream):
+                fits = self._fits()
+                lens = torch.where(fits, self._tokens if lens is None else lens, self._tokens + 1).int()  # refused, flagged
+                start = torch.where(fits, start, -1)                                                      # zeros
         for cell in self.cells:
             loop, layer = divmod(cell, kv.num_layers)
+            rows = dict(new_lens=lens, err_flag=self.err_flag, stream=stream)
             args = dict(new_lens=self.lens, err_flag=self.err_flag, stream=stream)
             if kv.plan_codes[cell] == LOOPKV_CELL_REUSE:
                 kr = self._rows["k"]
-                loopkv_norm_rope(self.rotary[layer], self.q[cell], self.k[cell], self.start, q_out=qr, k_out=kr, **args)
-                loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, self.start, sm_scale=self.sm_scale,
+                loopkv_norm_rope(self.rotary[layer], self.q[cell], self.k[cell], self.start, q_out=qr, k_out=kr, **rows)
+                loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, start, sm_scale=self.sm_scale,
                                        out=self.out[cell], max_seq_len=self.max_seq_len, k_cur=kr, v_cur=self.v[cell], **args)
             else:
                 loopkv_rope_append(kv, loop, layer, self.rotary[layer], self.q[cell], self.k[cell], self.v[cell],
-                                   self.block_table, self.start, q_out=qr, **args)
-                loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, self.start, sm_scale=self.sm_scale,
+                                   self.block_table, self.start, q_out=qr, **rows)
+                loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, start, sm_scale=self.sm_scale,
                                        out=self.out[cell], max_seq_len=self.max_seq_len, **args)
 
     def advance(self):
+        """Move start by the chunk, of sequences that it was stored of."""
         if not self.cells:
             return
-        new = self.q[self.cells[0]].shape[1] if self.lens is None else self.lens
-        self.start.add_((self.start >= 0) * new)
+        new = self._tokens if self.lens is None else self.lens
+        self.start.add_(torch.where(self._fits() & (self.start >= 0), new, 0).int())
