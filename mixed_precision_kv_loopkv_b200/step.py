@@ -58,7 +58,8 @@ class LoopedDecodeStep:
     """Sequences the per-cell kernels of one decode step (graph-capturable).
 
     pos    : device int32[B], current length n of every sequence (the new
-             token's position); ``advance()`` moves it by one on the device.
+             token's position); ``advance()`` moves it by one on the device,
+             on the stream of the last ``run`` unless another is given.
     q      : per cell, bf16[B, H, D]  (H query heads)
     k_new, v_new : per cell, bf16[B, 1, Hkv, D]: the token's K/V as the cell's
              loop computed it (appended by stored cells, attended exactly by
@@ -85,6 +86,7 @@ class LoopedDecodeStep:
         self.tau, self.sm_scale, self.max_seq_len = tau, sm_scale, max_seq_len
         self.sel_count = sel_count
         self.err_flag = err_flag
+        self._stream = None  # of the last run
 
     def launches_per_step(self) -> int:
         stored = sum(1 for c in self.cells if self.kv.plan_codes[c] != LOOPKV_CELL_REUSE)
@@ -94,7 +96,7 @@ class LoopedDecodeStep:
         """Enqueue the step.  Re-running it at the same positions rewrites
         the same bytes, so a warm-up run before capture leaves the cache
         state unchanged."""
-        kv = self.kv
+        kv, self._stream = self.kv, stream
         for cell in self.cells:
             kind = kv.plan_codes[cell]
             loop, layer = divmod(cell, kv.num_layers)
@@ -120,9 +122,10 @@ class LoopedDecodeStep:
                                     sel_count=None if self.sel_count is None else self.sel_count[cell],
                                     err_flag=self.err_flag, stream=stream, k_cur=cur_k, v_cur=cur_v)
 
-    def advance(self):
-        self.pos.add_(1)
-        self.pos_next.add_(1)
+    def advance(self, stream=None):
+        with _on(stream or self._stream):
+            self.pos.add_(1)
+            self.pos_next.add_(1)
 
     def capture(self, steps_per_graph: int = 1) -> torch.cuda.CUDAGraph:
         """Capture ``steps_per_graph`` consecutive steps (run + advance)."""
@@ -143,7 +146,8 @@ class LoopedChunkStep:
     and none of its cells stores or answers anything (its rows are zeros).
 
     start   : device int32[B], stored tokens of every sequence (negative: the
-              sequence is skipped); ``advance()`` moves it by the chunk
+              sequence is skipped); ``advance()`` moves it by the chunk, on the
+              stream of the last ``run`` unless another is given
     lens    : device int32[B], the sequences' new tokens, or None (all T)
     q, k, v : per cell, bf16 [B, T, H, D] and [B, T, Hkv, D] before norm and
               rotation, strided views of a projection included
@@ -159,6 +163,7 @@ class LoopedChunkStep:
         if len(self.rotary) != kv.num_layers:
             raise ValueError("one rotary for all layers or one for each")
         self.sm_scale, self.max_seq_len, self.err_flag = sm_scale, max_seq_len, err_flag
+        self._stream = None  # of the last run
         self.cells = list(range(len(kv.plan_codes))) if cells is None else sorted(cells)
         # rotated queries (and a reuse cell's keys): one cell's at a time
         shapes = {"q": self.q[self.cells[0]].shape, "k": self.k[self.cells[0]].shape} if self.cells else {}
@@ -189,7 +194,7 @@ class LoopedChunkStep:
         """Enqueue the chunk.  Not to be run twice at the same place without
         ``advance()``: storing a chunk completes key groups whose exact keys the
         chunk's own last tokens then replace."""
-        kv, qr = self.kv, self._rows.get("q")
+        kv, qr, self._stream = self.kv, self._rows.get("q"), stream
         lens, start = self.lens, self.start
         if self._guard and self.cells:
             with _on(stream):
@@ -211,9 +216,10 @@ class LoopedChunkStep:
                 loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, start, sm_scale=self.sm_scale,
                                        out=self.out[cell], max_seq_len=self.max_seq_len, **args)
 
-    def advance(self):
+    def advance(self, stream=None):
         """Move start by the chunk, of sequences that it was stored of."""
         if not self.cells:
             return
         new = self._tokens if self.lens is None else self.lens
-        self.start.add_(torch.where(self._fits() & (self.start >= 0), new, 0).int())
+        with _on(stream or self._stream):
+            self.start.add_(torch.where(self._fits() & (self.start >= 0), new, 0).int())

@@ -89,3 +89,30 @@ def test_all_tokens_without_lengths(m):
     step.advance()
     assert start.tolist() == [40, 31, -1]
     assert all(o[0].any() and not o[1:].any() for o in step.out.values())
+
+
+def test_run_and_advance_on_another_stream(m):
+    """Steps on a stream that has work before them: positions move when the calls
+    before have read them."""
+    B, T = 3, 10
+    want_kv, want_start, want = make(m, B, T, 160, 400)
+    kv, start, step = make(m, B, T, 160, 400)
+    outs = []
+    for _ in range(4):
+        want.run()
+        outs.append({c: o.clone() for c, o in want.out.items()})
+        want.advance()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    for i in range(4):
+        step.run(stream=side)
+        if i < 3:
+            step.advance()
+    side.synchronize()
+    assert start.tolist() == [30] * B and want_start.tolist() == [40] * B
+    for c in range(6):
+        assert torch.equal(step.out[c], outs[3][c])
+        if kv.arenas[c] is not None:
+            assert torch.equal(kv.arenas[c], want_kv.arenas[c])
