@@ -26,6 +26,12 @@
  *   - input rows may be strided (views of one fused projection), see loopkv_rows;
  *     outputs are contiguous.  An output must not overlap an input, except that
  *     q_out (k_out) may be q (k) itself where that is contiguous;
+ *   - a cell can go back (be appended to, or attended over, at fewer tokens than
+ *     it holds) to any place if it is bf16, and not below the last multiple of 32
+ *     tokens if it is 4-bit or 2-bit: behind that lie completed key groups, whose
+ *     exact keys are gone.  Drafted tokens that may be rejected are therefore
+ *     not appended but given as k_cur, v_cur, and the accepted ones appended
+ *     afterwards;
  *   - the launches are ordinary ones, in stream order (LOOPKV_FLAG_PDL changes
  *     nothing here).  A loopkv_decode_attention with that flag reads old cache
  *     blocks before it waits, so it must not directly follow an append of

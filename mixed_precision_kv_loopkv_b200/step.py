@@ -141,7 +141,11 @@ class LoopedChunkStep:
     """A chunk of new tokens through every (loop, layer) cell, in order.
 
     Two launches a cell: loopkv_rope_append (reuse cells: loopkv_norm_rope) and
-    loopkv_chunk_attention.  A sequence whose chunk does not fit the block table
+    loopkv_chunk_attention.  Drafted tokens, of which some may be rejected, must
+    not be stored before that is known (a 4-bit or 2-bit cell cannot go back
+    behind a key group that it has completed): ``run(store=False)`` attends with
+    the chunk's own exact rows in every cell and stores nothing, then lens is set
+    to what was accepted, and ``store()`` and ``advance()`` follow.  A sequence whose chunk does not fit the block table
     or a layer's rotation table, or whose length is outside [0, T], is flagged,
     and none of its cells stores or answers anything (its rows are zeros).
 
@@ -176,9 +180,10 @@ class LoopedChunkStep:
         # Norms and appends skip a sequence that runs past its rotation table, which
         # the attention does not know of: it would read rows that were never
         # written.  Where a table does not reach as far as the attention answers
-        # (a reuse cell: the chunk behind a full cell), both are told beforehand.
-        reuse = any(kv.plan_codes[c] == LOOPKV_CELL_REUSE for c in self.cells)
-        self._guard = positions < capacity + (self._tokens if reuse else 0)
+        # (exact rows: a chunk behind a full cell), both are told beforehand, by some
+        # small operations that a table of capacity + T positions makes unnecessary.
+        self._positions, self._capacity = positions, capacity
+        self._reuse = any(kv.plan_codes[c] == LOOPKV_CELL_REUSE for c in self.cells)
 
     def launches_per_step(self) -> int:
         return 2 * len(self.cells)
@@ -190,22 +195,27 @@ class LoopedChunkStep:
         n = self.lens
         return (n == 0) | ((n > 0) & (n <= self._tokens) & (self.start <= self._limit - n))
 
-    def run(self, stream=None):
+    def _guarded(self, stream, exact: bool):
+        """lens for norms and appends (beyond all: refused and flagged) and start for
+        the attention (negative: zeros), where a chunk does not fit."""
+        if not self.cells or self._positions >= self._capacity + (self._tokens if exact else 0):
+            return self.lens, self.start
+        with _on(stream):
+            fits = self._fits()
+            lens = torch.where(fits, self._tokens if self.lens is None else self.lens, self._tokens + 1).int()
+            return lens, torch.where(fits, self.start, -1)
+
+    def run(self, stream=None, store: bool = True):
         """Enqueue the chunk.  Not to be run twice at the same place without
         ``advance()``: storing a chunk completes key groups whose exact keys the
         chunk's own last tokens then replace."""
         kv, qr, self._stream = self.kv, self._rows.get("q"), stream
-        lens, start = self.lens, self.start
-        if self._guard and self.cells:
-            with _on(stream):
-                fits = self._fits()
-                lens = torch.where(fits, self._tokens if lens is None else lens, self._tokens + 1).int()  # refused, flagged
-                start = torch.where(fits, start, -1)                                                      # zeros
+        lens, start = self._guarded(stream, self._reuse or not store)
         for cell in self.cells:
             loop, layer = divmod(cell, kv.num_layers)
             rows = dict(new_lens=lens, err_flag=self.err_flag, stream=stream)
             args = dict(new_lens=self.lens, err_flag=self.err_flag, stream=stream)
-            if kv.plan_codes[cell] == LOOPKV_CELL_REUSE:
+            if not store or kv.plan_codes[cell] == LOOPKV_CELL_REUSE:
                 kr = self._rows["k"]
                 loopkv_norm_rope(self.rotary[layer], self.q[cell], self.k[cell], self.start, q_out=qr, k_out=kr, **rows)
                 loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, start, sm_scale=self.sm_scale,
@@ -215,6 +225,17 @@ class LoopedChunkStep:
                                    self.block_table, self.start, q_out=qr, **rows)
                 loopkv_chunk_attention(kv, loop, layer, qr, self.block_table, start, sm_scale=self.sm_scale,
                                        out=self.out[cell], max_seq_len=self.max_seq_len, **args)
+
+    def store(self, stream=None):
+        """Store the chunk's first lens[b] tokens in every stored cell, after
+        ``run(store=False)``: the same bytes that ``run()`` of those tokens stores."""
+        kv, self._stream = self.kv, stream
+        lens, _ = self._guarded(stream, False)
+        for cell in self.cells:
+            loop, layer = divmod(cell, kv.num_layers)
+            if kv.plan_codes[cell] != LOOPKV_CELL_REUSE:
+                loopkv_rope_append(kv, loop, layer, self.rotary[layer], None, self.k[cell], self.v[cell], self.block_table,
+                                   self.start, new_lens=lens, err_flag=self.err_flag, stream=stream)
 
     def advance(self, stream=None):
         """Move start by the chunk, of sequences that it was stored of."""

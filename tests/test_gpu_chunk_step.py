@@ -116,3 +116,83 @@ def test_run_and_advance_on_another_stream(m):
         assert torch.equal(step.out[c], outs[3][c])
         if kv.arenas[c] is not None:
             assert torch.equal(kv.arenas[c], want_kv.arenas[c])
+
+
+@pytest.mark.parametrize("d,hkv", [(64, 2), (128, 4)])
+def test_drafted_tokens_are_checked_then_stored(m, d, hkv):
+    """Rounds of drafted tokens over key group borders: every row is the oracle's
+    over what was accepted before and its own draft, and the cells hold what they
+    would hold if no other token had ever been seen."""
+    B, T, H = 3, 20, 4
+    lens, err = ints([T] * B), ints([0])
+    kv, start, step = make(m, B, T, 160, 400, d=d, hkv=hkv, lens=lens, err_flag=err)
+    ref_kv, ref_start, ref = make(m, B, T, 160, 400, d=d, hkv=hkv, lens=ints([0] * B))
+    rotary, have = step.rotary[0], [0] * B
+    kept = {c: [[[], []] for _ in range(B)] for c in range(6)}     # rotated keys and values of the accepted
+    weight = host(rotary.k_weight)
+    table = host(rotary.table)
+    for turn, (drafted, accepted) in enumerate([([20, 17, 20], [20, 17, 3]), ([20, 20, 5], [13, 1, 5]), ([9, 20, 20], [0, 15, 20]),
+                                                ([20, 20, 20], [1, 14, 7]), ([20, 1, 20], [11, 1, 19])]):
+        for c in range(6):
+            x = fused_rows(B, T, H, hkv, d, 1000 * turn + c)
+            for s in (step, ref):
+                s.q[c], s.k[c], s.v[c] = x
+        lens.copy_(ints(drafted))
+        before = [None if a is None else a.clone() for a in kv.arenas]
+        step.run(store=False)
+        assert all(a is None or torch.equal(a, b) for a, b in zip(kv.arenas, before))
+        for c in range(6):
+            src = c + N if PLAN[c] == "reuse" else c
+            for b, n in enumerate(drafted):
+                pos = have[b] + torch.arange(n).numpy()
+                qr = CO.norm_rope(host(step.q[c][b, :n]), pos, table)
+                kr = CO.norm_rope(host(step.k[c][b, :n]), pos, table, weight=weight)
+                for h in range(H):
+                    j = h * hkv // H
+                    old = [torch.cat([torch.zeros(0, hkv, d)] + x).numpy()[:, j] for x in kept[src][b]]
+                    kh, vh = CO.stored_values(PLAN[src], *old)
+                    kh = torch.cat([torch.from_numpy(kh), torch.from_numpy(kr[:, j]).double()]).numpy()
+                    vh = torch.cat([torch.from_numpy(vh), step.v[c][b, :n, j].cpu().double()]).numpy()
+                    want, slack = CO.chunk_attend(qr[:, h], kh, vh, pos, 0.3)
+                    assert (abs(host(step.out[c][b, :n, h]) - want) <= slack).all(), (turn, c, b, h)
+        for c in range(6):
+            for b, n in enumerate(accepted):
+                pos = have[b] + torch.arange(n).numpy()
+                kept[c][b][0].append(torch.from_numpy(CO.norm_rope(host(step.k[c][b, :n]), pos, table, weight=weight)))
+                kept[c][b][1].append(step.v[c][b, :n].float().cpu())
+        for x in (lens, ref.lens):
+            x.copy_(ints(accepted))
+        step.store()
+        step.advance()
+        ref.run()
+        ref.advance()
+        have = [a + n for a, n in zip(have, accepted)]
+        assert start.tolist() == have == ref_start.tolist()
+        for c in range(6):
+            if kv.arenas[c] is not None:
+                assert torch.equal(kv.arenas[c], ref_kv.arenas[c])
+                if kv.residuals[c] is not None:
+                    for b, n in enumerate(have):
+                        assert torch.equal(kv.residuals[c][b, :, : n % 32], ref_kv.residuals[c][b, :, : n % 32])
+    assert int(err) == 0
+
+
+def test_how_far_a_cell_can_go_back(m):
+    """A quantised cell appended to again from the last multiple of 32 tokens on,
+    a bf16 cell from anywhere, holds what it would hold without the rejected tokens."""
+    rows = [fused_rows(1, 100, 4, 2, 64, seed) for seed in (1, 2)]
+    for kind, back in (("q4", 64), ("q4", 70), ("q2", 64), ("bf16", 3), ("bf16", 50)):
+        got, want = (m.KVCells([kind], 1, 1, 4, 64, 8, 1, 8, num_kv_heads=2) for _ in range(2))
+        table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+        (_, k1, v1), (_, k2, v2) = rows
+
+        def append(kv, k, v, at, lo, hi):
+            m.loopkv_rope_append(kv, 0, 0, None, None, k[:, lo:hi], v[:, lo:hi], table, ints([at]))
+
+        append(got, k1, v1, 0, 0, 75)
+        append(got, k2, v2, back, 0, 40)
+        append(want, k1, v1, 0, 0, back)
+        append(want, k2, v2, back, 0, 40)
+        n = back + 40
+        for a, b in zip(*(m.loopkv_read_tokens(kv, 0, 0, table, ints([n]), ints([0]), n) for kv in (got, want))):
+            assert torch.equal(a, b), (kind, back)
