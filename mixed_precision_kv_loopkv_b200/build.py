@@ -8,6 +8,7 @@ process that already holds a CUDA context (PyTorch's included).
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -26,6 +27,28 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "-cudart", "static",
 ]
+
+# Kernels whose groups of warps move registers between them share out what the
+# launch gave (ChunkRegs in chunk_tensor.cuh): built with fewer a thread, the
+# groups that take some would wait for good.  {source: (kernel, registers)}
+LAUNCH_REGISTERS = {"chunk_attention.cu": (r"chunk_tensor_kernelILi\dELi\d+ELi2E", 96)}
+
+
+def check_registers(source: str, ptxas: str) -> int:
+    """Compare ptxas' report (-v) with LAUNCH_REGISTERS; the number of kernels compared."""
+    if source not in LAUNCH_REGISTERS:
+        return 0
+    kernel, want = LAUNCH_REGISTERS[source]
+    found = 0
+    for name, used in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", ptxas, re.S):
+        if not re.search(kernel, name):
+            continue
+        if int(used) != want:
+            raise RuntimeError(f"{source}: {name} uses {used} registers, its register split needs {want}")
+        found += 1
+    if not found:
+        raise RuntimeError(f"{source}: no kernel like {kernel} in the compiler's report")
+    return found
 
 
 def _nvcc() -> str:
@@ -52,10 +75,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(build_dir, exist_ok=True)
     for src in SOURCES:
         obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
-        cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-Xptxas", "-v" if verbose else "-O3",
-               "-c", os.path.join(CSRC, src), "-o", obj]
-        subprocess.run(cmd, check=True, stdout=None if verbose else subprocess.DEVNULL,
-                       stderr=None if verbose else subprocess.PIPE)
+        cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-Xptxas", "-v", "-c", os.path.join(CSRC, src), "-o", obj]
+        done = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        if verbose or done.returncode:
+            print(done.stdout, file=sys.stderr)
+        done.check_returncode()
+        check_registers(src, done.stdout)
         objs.append(obj)
     tmp = LIB + ".tmp"
     subprocess.run([_nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a",

@@ -53,19 +53,15 @@ cudaError_t launch_clusters(Kernel kern, int64_t units, int splits, int threads,
   return cudaLaunchKernelEx(&cfg, kern, p, args..., splits);
 }
 
-// Shared-memory limit of a kernel (MT < 0: of -MT warps, for few rows), once a device;
-// regs: registers that it must have been built with (0: any).
+// Shared-memory limit of a kernel (MT < 0: of -MT warps, for few rows), once a device.
 template <int KIND, int D, int MT, typename Kernel>
-cudaError_t prepare_once(Kernel kern, size_t smem, int regs, int dev) {
+cudaError_t prepare_once(Kernel kern, size_t smem, int dev) {
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && done[dev]) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes attr;
-  if (regs && (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != regs))
-    return cudaErrorInvalidConfiguration;
   if (dev >= 0) done[dev] = true;
   return cudaSuccess;
 }
@@ -103,9 +99,8 @@ cudaError_t launch_mt(const ChunkAttnParams& p, cudaStream_t stream) {
   constexpr size_t kSmem = MT * (2 * kStepKeys + D) > 256 && L::kBytes < 120 * 1024 ? 120 * 1024 : L::kBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
   const int dev = current_device();
-  // the registers that the groups of warps pass on are those of the launch
   static constexpr auto kern = chunk_tensor_kernel<KIND, D, MT>;
-  const cudaError_t e = prepare_once<KIND, D, MT>(kern, kSmem, ChunkRegs<MT>::kMoves ? ChunkRegs<MT>::kLaunch : 0, dev);
+  const cudaError_t e = prepare_once<KIND, D, MT>(kern, kSmem, dev);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.chunk.T) << p.g_log2;
   const int64_t row_tiles = (rows + MT * 128 - 1) / (MT * 128);
@@ -128,7 +123,7 @@ cudaError_t few_w(const ChunkAttnParams& p, int64_t units, int64_t groups, int d
   using L = FewSmem<KIND, D, WARPS>;
   static_assert(kFewWarpsPerSm / WARPS * (L::kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
   static constexpr auto kern = chunk_few_kernel<KIND, D, WARPS>;
-  const cudaError_t e = prepare_once<KIND, D, -WARPS>(kern, L::kBytes, 0, dev);
+  const cudaError_t e = prepare_once<KIND, D, -WARPS>(kern, L::kBytes, dev);
   if (e != cudaSuccess) return e;
   if (!best) return launch_clusters(kern, units, *splits, WARPS * 32, L::kBytes, stream, p);
   auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };

@@ -132,12 +132,13 @@ __host__ __device__ constexpr int chunk_threads() { return (MT * 4 + kBlockWarps
 // Registers a thread after the split.  They come out of what the block was
 // launched with, 65536 / threads rounded down to a multiple of 8 a thread:
 // MT = 2: 5 groups of 96 >= 2 x 128 + 2 x 88 + 48.  MT = 1: 4 of 128 each, as launched.
+// (The build compares the 96 with what the compiler used.)
 template <int MT>
 struct ChunkRegs {
   static constexpr int kSoftmax = 128, kDequant = MT == 2 ? 88 : 128, kIssue = MT == 2 ? 48 : 128;
   static constexpr int kLaunch = 65536 / chunk_threads<MT>() / 8 * 8;
-  static constexpr bool kMoves = MT == 2;
   static_assert(MT * kSoftmax + 2 * kDequant + kIssue <= (MT + 3) * kLaunch, "register split");
+  static_assert(MT == 1 || kLaunch == 96, "LAUNCH_REGISTERS of build.py");
 };
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }

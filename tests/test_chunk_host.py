@@ -227,3 +227,23 @@ def test_capacity_beyond_31_bits_is_unsupported(m, c):
 
 def test_scale_that_overflows_is_invalid(m, c):
     assert _attend(m, c, _cfg(m, [Q4], 1, 1), _cells(m, 1), sm_scale=3e38) == 1
+
+
+def test_build_refuses_other_register_counts():
+    """The register split of the 256-row kernels is compared with what the compiler
+    used, when the library is built and not when a user calls it."""
+    from mixed_precision_kv_loopkv_b200 import build
+    source = "chunk_attention.cu"
+
+    def report(*kernels):
+        return "".join(f"ptxas info    : Compiling entry function '{name}' for 'sm_100a'\nptxas info    : Function properties "
+                       f"for {name}\n    0 bytes stack frame\nptxas info    : Used {regs} registers, used 1 barriers\n"
+                       for name, regs in kernels)
+
+    good = [("_ZN6loopkv19chunk_tensor_kernelILi0ELi128ELi2EEEvNS", 96), ("_ZN6loopkv19chunk_tensor_kernelILi3ELi64ELi2EEEvNS", 96)]
+    others = [("_ZN6loopkv19chunk_tensor_kernelILi0ELi128ELi1EEEvNS", 127), ("_ZN6loopkv16chunk_few_kernelILi0ELi128ELi12EEEvNS", 168)]
+    assert build.check_registers(source, report(others[0], *good, others[1])) == 2
+    assert build.check_registers("append.cu", "") == 0
+    for bad in (report(good[0], (good[1][0], 88)), report((good[0][0], 104), good[1]), report(*others), ""):
+        with pytest.raises(RuntimeError):
+            build.check_registers(source, bad)
