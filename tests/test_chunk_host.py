@@ -247,3 +247,25 @@ def test_build_refuses_other_register_counts():
     for bad in (report(good[0], (good[1][0], 88)), report((good[0][0], 104), good[1]), report(*others), ""):
         with pytest.raises(RuntimeError):
             build.check_registers(source, bad)
+
+
+def test_polynomial_exponential():
+    """The cubic of the softmax' FMA units: 7.5e-5 of 2^x at the most (its steps in
+    fp32, each multiply-add rounded once), over every fraction and many exponents."""
+    text = open(os.path.join(ROOT, "mixed_precision_kv_loopkv_b200", "csrc", "chunk_tensor.cuh")).read()
+    body = text[text.index("void poly_exp2("):]
+    body = body[:body.index("\n}\n")]
+    c3, c2, c1, c0 = (np.float32(x) for x in re.findall(r"pack2\((\d\.\d+e-\d+)f, \1f\)", body))
+    x = np.concatenate([np.linspace(-126, 100, 400_001), np.linspace(-1, 1, 400_001)]).astype(np.float32)
+    magic = np.float32(12582912.0)
+    n = (x + magic) - magic
+
+    def fma(a, b, c):
+        return (a.astype(np.float64) * b + np.float64(c)).astype(np.float32)   # exact product, one rounding to 53, one to 24 bits
+
+    f = (x.astype(np.float64) - n).astype(np.float32)
+    assert np.abs(f).max() <= 0.5
+    y = fma(fma(fma(f, c3, c2), f, c1), f, c0)
+    got = np.ldexp(y.astype(np.float64), n.astype(np.int64))
+    rel = np.abs(got / np.exp2(x.astype(np.float64)) - 1)
+    assert 7e-5 < rel.max() < 7.6e-5

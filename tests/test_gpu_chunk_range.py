@@ -130,3 +130,37 @@ def test_keys_queries_and_scale_far_from_one(m, kind, current, T, start, k_pow, 
         k.mul_(2.0**k_pow)
         q.mul_(2.0**q_pow)
     far_case(m, kind, 64, T, start, current, change, seed=12, sm=0.5 * 2.0**s_pow, rows=range(0, T, max(1, T // 9)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [1, 2])
+def test_all_columns_weigh_alike(m, d, heads):
+    """Keys of one logit have one weight, whether its exponential is the unit's or
+    the polynomial's (columns 6 and 7 of eight), over many fractions of the exponent.
+
+    Values 1 in six columns and -3 in two cancel: with w the keys' weight beside one
+    of weight 1, 48 n (w' - w'') / (1 + 64 n w) remains of n x 64 keys, where w' and w''
+    differ by 7.6e-5 (the cubic) + 2 x 2^-11 (both rounded to fp16) + 2^-20 (the unit,
+    sums) of w; then the output's rounding.
+    """
+    T, n = 150, 3
+    k = torch.zeros(1, 64 * n + 8, 1, d, device="cuda")
+    v = torch.zeros_like(k)
+    k[:, 1:8, :, 0] = -60000.0                  # no weight; key 0, of logit 0, comes first and is the reference
+    k[:, 8:, :, 0] = -1
+    v[:, 8:] = torch.where(torch.arange(64 * n, device="cuda") % 8 < 6, 1.0, -3.0)[None, :, None, None]
+    k, v = k.bfloat16(), v.bfloat16()
+    q = torch.zeros(1, T, heads, d, device="cuda")
+    q[0, :, :, 0] = torch.linspace(0.01, 4, T, device="cuda")[:, None] + 0.013 * torch.arange(heads, device="cuda")
+    q = q.bfloat16()
+    cur = torch.zeros(1, T, 1, d, dtype=torch.bfloat16, device="cuda")
+    kc = cur.clone()
+    kc[..., 0] = -60000.0                       # the chunk's own rows: no weight
+    kv, table = cell_for(m, "bf16", 1, 1, d, 64 * n + 8, heads)
+    m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0]))
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([64 * n + 8]), sm_scale=1.0, k_cur=kc, v_cur=cur)
+    w = np.exp(-host(q[0, :, :, 0]).astype(np.float64))
+    bound = 48 * n * w * (7.6e-5 + 2 * 2.0**-11 + 2.0**-20) / (1 + 64 * n * w * (1 - 2.0**-9)) * (1 + 2.0**-8)
+    off = np.abs(host(out[0])).max(-1)
+    assert np.all(off <= bound), float((off / bound).max())
+    assert off.max() > 0                        # the two do differ
