@@ -535,13 +535,11 @@ __global__ void __launch_bounds__(WARPS * 32, kFewWarpsPerSm / WARPS) chunk_few_
   __syncwarp();
   const OddRange odd = *reinterpret_cast<const OddRange*>(smem + L::kOdd + warp * 16);
   if (ok && odd.first < odd.end) {
-    const int start = p.chunk.start_pos[at.b], stored = start + (p.k_cur.p ? 0 : tokens);
-#pragma unroll 1
-    for (int i = lane; i < rows * D; i += 32) {
-      const int t = (i / D) >> p.g_log2;
-      out[i] += odd_values<KIND, D>(p, at.b, at.hk, p.k_cur.p ? start : start + t + 1, t + 1,
-                                    (stored + kGroup - 1) / kGroup * kGroup, odd, i % D);
-    }
+    const int start = p.chunk.start_pos[at.b], stored = start + (p.k_cur.p ? 0 : tokens), t = lane >> p.g_log2;
+    OddSum<D> sum;
+    odd_values<KIND, D>(p, at.b, at.hk, start + (p.k_cur.p ? 0 : t + 1), t + 1, tokens,
+                        (stored + kGroup - 1) / kGroup * kGroup, odd, sum);
+    if (lane < rows) add_odd<D>(sum, [&](int c, float v) { out[lane * D + c] += v; });
   }
   __syncthreads();
   constexpr int kQuads = D / 4;

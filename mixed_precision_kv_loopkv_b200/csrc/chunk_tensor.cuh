@@ -294,39 +294,88 @@ __device__ __forceinline__ void note_odd_keys(uint32_t odd_at, int first, int co
   asm volatile("red.shared::cta.max.s32 [%0], %1;" ::"r"(odd_at + 4), "r"(first + count) : "memory");
 }
 
-// Value c of stored token t, as read_tokens gives it but not rounded.
+// The infinities that a row's channels get from the values that are not finite:
+// of both signs, or a NaN, in one channel is NaN.
+template <int D>
+struct OddSum {
+  uint32_t plus[D / 32], minus[D / 32];
+};
+
+// Those of odd's keys, for a whole warp, a row a lane: it sees `stored` stored
+// tokens and `current` current rows.  Current rows count from key0 on; there are
+// len of them.  Blocks without such values cost one look at their scales (their
+// rows), the others two votes for each token and 32 channels, however many they are.
 template <int KIND, int D>
-__device__ float stored_value(const ChunkAttnParams& p, int b, int hk, int t, int c) {
+__device__ __forceinline__ void odd_values(const ChunkAttnParams& p, int b, int hk, int stored, int current, int len, int key0,
+                                           OddRange odd, OddSum<D>& sum) {
   using R = Rec<KIND, D>;
-  const int phys = p.block_table[static_cast<size_t>(b) * p.max_blocks + t / kBlock], row = t % kBlock;
-  const uint8_t* rec = p.arena + (static_cast<size_t>(phys) * p.Hkv + hk) * R::kBytes;
-  if constexpr (KIND == LOOPKV_CELL_BF16) {
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rec + R::kBfV)[row * D + c]);
-  } else {
-    const uint32_t m = *reinterpret_cast<const uint32_t*>(rec + R::kVMetaOff + (row * (D / kGroup) + c / kGroup) * 4);
-    uint32_t code = (rec[R::kVHi + c / 4 * kBlock + row] >> (2 * (c % 4))) & 3u;
-    if constexpr (KIND == LOOPKV_CELL_Q4) code = code << 2 | ((rec[R::kQ4VLo + row * R::kRow + c / 4] >> (2 * (c % 4))) & 3u);
-    return fmaf(bf16_lo(m), static_cast<float>(code), bf16_hi(m));
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) sum.plus[w] = sum.minus[w] = 0u;
+#pragma unroll 1
+  for (int i = odd.first; i < odd.end; i += kBlock) {
+    const bool exact = KIND == LOOPKV_CELL_BF16 || i >= key0;
+    const uint8_t* rec = nullptr;
+    if (i < key0) {
+      const int phys = p.block_table[static_cast<size_t>(b) * p.max_blocks + min(i / kBlock, p.max_blocks - 1)];
+      if (phys < 0 || phys >= p.num_blocks) continue;  // no block there: behind the last token
+      rec = p.arena + (static_cast<size_t>(phys) * p.Hkv + hk) * R::kBytes;
+    }
+    auto row_of = [&](int t) {  // an exact row, or null
+      if (i < key0) return reinterpret_cast<const __nv_bfloat16*>(rec + R::kBfV) + t * D;
+      return i - key0 + t < len ? row_at(p.v_cur, b, i - key0 + t, hk) : nullptr;
+    };
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(rec + R::kVMetaOff);  // [token][D / 32]
+    bool some = false;
+    if (exact) {
+#pragma unroll 1
+      for (int k = lane; k < kBlock * (D / 8); k += 32) {
+        const __nv_bfloat16* row = row_of(k / (D / 8));
+        if (!row) continue;
+        const uint4 x = reinterpret_cast<const uint4*>(row)[k % (D / 8)], f = finite_bf16x8(x);
+        some = some || x.x != f.x || x.y != f.y || x.z != f.z || x.w != f.w;
+      }
+    } else {
+#pragma unroll 1
+      for (int k = lane; k < kBlock * (D / kGroup); k += 32) some = some || odd_meta(meta[k]);
+    }
+    if (!__any_sync(0xffffffffu, some)) continue;
+#pragma unroll 1
+    for (int t = 0; t < kBlock; ++t) {
+      const bool seen = i < key0 ? i + t < stored : i - key0 + t < current;
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        float v = 0.f;
+        if (exact) {
+          const __nv_bfloat16* row = row_of(t);
+          if (row) v = __bfloat162float(row[32 * w + lane]);
+        } else {
+          const uint32_t m = meta[t * (D / kGroup) + w];
+          if (odd_meta(m)) {  // min + scale x code, as read_tokens gives it
+            const int c = 32 * w + lane;
+            uint32_t code = (rec[R::kVHi + c / 4 * kBlock + t] >> (2 * (c % 4))) & 3u;
+            if constexpr (KIND == LOOPKV_CELL_Q4) code = code << 2 | ((rec[R::kQ4VLo + t * R::kRow + c / 4] >> (2 * (c % 4))) & 3u);
+            v = fmaf(bf16_lo(m), static_cast<float>(code), bf16_hi(m));
+          }
+        }
+        const uint32_t plus = __ballot_sync(0xffffffffu, !(v < INFINITY)), minus = __ballot_sync(0xffffffffu, !(v > -INFINITY));
+        if (seen) sum.plus[w] |= plus, sum.minus[w] |= minus;
+      }
+    }
   }
 }
 
-// What those of odd's keys add to channel c of a row that sees `stored` stored
-// tokens and `current` current rows: 0, an infinity or NaN.  Current rows count
-// from key0 on.
-template <int KIND, int D>
-__device__ __forceinline__ float odd_values(const ChunkAttnParams& p, int b, int hk, int stored, int current, int key0,
-                                         OddRange odd, int c) {
-  float sum = 0.f;
-  for (int i = odd.first; i < odd.end; ++i) {
-    float v = 0.f;
-    if (i < key0) {
-      if (i < stored) v = stored_value<KIND, D>(p, b, hk, i, c);
-    } else if (i - key0 < current) {
-      v = __bfloat162float(row_at(p.v_cur, b, i - key0, hk)[c]);
+// Each channel that gets any: add(channel, what).
+template <int D, typename Add>
+__device__ __forceinline__ void add_odd(const OddSum<D>& sum, Add&& add) {
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {
+#pragma unroll 1
+    for (uint32_t left = sum.plus[w] | sum.minus[w]; left; left &= left - 1) {
+      const uint32_t bit = left & -left;
+      add(32 * w + __ffs(left) - 1, !(sum.minus[w] & bit) ? INFINITY : sum.plus[w] & bit ? NAN : -INFINITY);
     }
-    if (!isfinite(v)) sum += v;
   }
-  return sum;
 }
 
 // What the CTA works on.
@@ -1068,17 +1117,18 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
       }
       // (all blocks' notes came before the last values' arrival)
       const OddRange found{*reinterpret_cast<volatile int*>(&odd->first), *reinterpret_cast<volatile int*>(&odd->end)};
-      if (ok && valid && found.first < found.end) {
-        const int token = row >> p.g_log2, see = p.chunk.start_pos[at.b] + (p.k_cur.p ? 0 : token + 1);
-#pragma unroll 1
-        for (int c = 0; c < D; ++c) {
-          const float v = odd_values<KIND, D>(p, at.b, at.hk, see, token + 1, job.stored_tiles * kTileKeys, found, c);
-          if (v == 0.f) continue;
-          if (splits == 1)
-            o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + v);
-          else
-            reinterpret_cast<float*>(smem + L::kPartial + local * D * 4 + (((c / 4) ^ (local & (D / 4 - 1))) << 4))[c % 4] += v;
-        }
+      if (ok && found.first < found.end) {
+        const int token = row >> p.g_log2, start = p.chunk.start_pos[at.b];
+        OddSum<D> sum;
+        odd_values<KIND, D>(p, at.b, at.hk, start + (p.k_cur.p ? 0 : token + 1), token + 1, rows >> p.g_log2,
+                            job.stored_tiles * kTileKeys, found, sum);
+        if (valid)
+          add_odd<D>(sum, [&](int c, float v) {
+            if (splits == 1)
+              o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + v);
+            else
+              reinterpret_cast<float*>(smem + L::kPartial + local * D * 4 + (((c / 4) ^ (local & (D / 4 - 1))) << 4))[c % 4] += v;
+          });
       }
     }
   }

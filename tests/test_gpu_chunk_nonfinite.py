@@ -287,3 +287,22 @@ def test_a_quantised_key_group_that_is_not_finite(m, kind, T, start):
         for h in range(2):
             want, slack = attend_any(host(q[b, :, h]).astype(np.float64), kh, vh, start + np.arange(T), 0.6)
             check(out[b, :, h], want, slack, (b, h))
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2", "bf16"])
+@pytest.mark.parametrize("T", [6, 150])
+@pytest.mark.parametrize("every", [1, 9000])
+def test_many_values_that_are_not_finite(m, kind, T, every):
+    """Infinities in one channel group of all tokens, or far apart, in a long context."""
+    n, d = 18_100, 64
+    kv, table = cell_for(m, kind, 1, 1, d, n)
+    k, v, q = (seeded_bf16((1, n, 1, d), i) for i in range(3))
+    v[:, ::every, :, 32:] = INF
+    m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0]))
+    q = q[:, :T].contiguous()
+    out = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([n - T]), sm_scale=0.1)
+    v[:, ::every, :, 32:] = 0
+    m.loopkv_rope_append(kv, 0, 0, None, None, k, v, table, ints([0]))
+    want = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([n - T]), sm_scale=0.1)
+    assert torch.equal(out[..., :32], want[..., :32])
+    assert torch.isnan(out[..., 32:]).all() if kind != "bf16" else torch.isposinf(out[..., 32:]).all()
