@@ -48,9 +48,10 @@ def prefill(kv: KVCells, loop: int, layer: int, k, v, block_table, lens, err_fla
         if cut <= prev:
             continue
         starts = [prev if n >= cut else -1 for n in lens]
-        pos = torch.tensor(starts, dtype=torch.int32, device=k.device)
-        loopkv_quantize_append(kv, loop, layer, k[:, prev:cut].contiguous(), v[:, prev:cut].contiguous(),
-                               block_table, pos, err_flag=err_flag, stream=stream)
+        with _on(stream):  # the copies are made where they are read
+            pos = torch.tensor(starts, dtype=torch.int32, device=k.device)
+            loopkv_quantize_append(kv, loop, layer, k[:, prev:cut].contiguous(), v[:, prev:cut].contiguous(),
+                                   block_table, pos, err_flag=err_flag, stream=stream)
         prev = cut
 
 

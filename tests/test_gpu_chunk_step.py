@@ -196,3 +196,53 @@ def test_how_far_a_cell_can_go_back(m):
         n = back + 40
         for a, b in zip(*(m.loopkv_read_tokens(kv, 0, 0, table, ints([n]), ints([0]), n) for kv in (got, want))):
             assert torch.equal(a, b), (kind, back)
+
+
+def test_prefill_on_another_stream(m):
+    """The rows that prefill copies and the positions that it makes are read when
+    they are there, on a stream that is behind and beside one that is busy."""
+    k, v = seeded_bf16((3, 90, 2, 64), 1), seeded_bf16((3, 90, 2, 64), 2)
+    kvs = [m.KVCells(["q4"], 1, 1, 2, 64, 24, 3, 8) for _ in range(2)]
+    table = torch.arange(24, dtype=torch.int32, device="cuda").view(3, 8)
+    lens = [90, 33, 70]
+    m.prefill(kvs[0], 0, 0, k, v, table, lens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)          # the current stream's own work
+    m.prefill(kvs[1], 0, 0, k, v, table, lens, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(kvs[0].arenas[0], kvs[1].arenas[0])
+
+
+def test_a_captured_step_replays_chunk_after_chunk(m):
+    """run and advance in one graph: each replay is the next chunk of what its
+    buffers then hold."""
+    B, T = 3, 12
+    lens, err = ints([T] * B), ints([0])
+    kv, start, step = make(m, B, T, 160, 160, lens=lens, err_flag=err)
+    ref_kv, ref_start, ref = make(m, B, T, 160, 160, lens=ints([T] * B))
+    start.fill_(-1)
+    step.run()                               # warm-up: every sequence is skipped
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run()
+        step.advance()
+    start.fill_(0)
+    for turn, n in enumerate([[12, 1, 7], [12, 12, 0], [5, 12, 12], [12, 12, 12], [1, 2, 12]]):
+        for x in (lens, ref.lens):
+            x.copy_(ints(n))
+        for c in range(6):
+            x = fused_rows(B, T, 4, 2, 64, 100 * turn + c)
+            for held, new in zip((step.q[c], step.k[c], step.v[c]), x):
+                held.copy_(new)
+            ref.q[c], ref.k[c], ref.v[c] = x
+        graph.replay()
+        ref.run()
+        ref.advance()
+        assert start.tolist() == ref_start.tolist()
+        for c in range(6):
+            for b in range(B):
+                assert torch.equal(step.out[c][b, : n[b]], ref.out[c][b, : n[b]])
+            assert kv.arenas[c] is None or torch.equal(kv.arenas[c], ref_kv.arenas[c])
+    assert int(err) == 0

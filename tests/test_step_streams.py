@@ -49,3 +49,10 @@ def test_advance_follows_the_stream_of_the_run(step_module, which):
     x.run()
     x.advance()
     assert used == ["side", "other", None]
+
+
+def test_prefill_copies_on_the_stream_of_its_appends(step_module):
+    step, used = step_module
+    k = torch.zeros(2, 9, 1, 64, dtype=torch.bfloat16)
+    step.prefill(Cells(), 0, 0, k, k, None, [9, 4], stream="side")
+    assert used == ["side", "side"]
