@@ -21,7 +21,8 @@
 //   append of 8191 tokens, 16 heads of 128, 4-bit, queries rotated: 59 us for
 //   155 MB; instruction issue (the quantiser and the rotation); with 64
 //   registers and eight CTAs an SM (72 and seven: 60 us; rows unrolled four
-//   times, 94 registers: 91 us, the code outgrows the instruction cache)
+//   times, 94 registers: 91 us, the code outgrows the instruction cache); heads
+//   of 128 spill 8 to 12 bytes a thread
 //   append of 64 x 1 token: 8.0 us, five dependent round trips
 #include "append_ops.cuh"
 #include "chunk_common.cuh"
@@ -62,7 +63,7 @@ __device__ __forceinline__ void load_turn(const RotaryView& r, int pos, int sub,
 // mantissa are moved into a double's, which costs two integer operations where
 // the conversion instruction runs at an eighth of their rate; 0 comes out as
 // 2^-127, whose square is nothing beside eps (at least 1e-30), and infinities and
-// NaN as 2^128 and more: a sum of 2^256, for which see any_huge.
+// NaN as 2^128 and more: a sum of 2^256, for which see kTinyNorm.
 __device__ __forceinline__ double add_squares(uint32_t w, double sum) {
   const double a = __hiloint2double(static_cast<int>((w & 0x7FFFu) * 8192u + 0x38000000u), 0);
   const double b = __hiloint2double(static_cast<int>(((w & 0x7FFF0000u) >> 3) + 0x38000000u), 0);
@@ -73,32 +74,11 @@ __device__ __forceinline__ double squares(const uint4& raw) {
   return add_squares(raw.w, add_squares(raw.z, add_squares(raw.y, add_squares(raw.x, 0.0))));
 }
 
-// The same with every number converted: infinite or NaN where an entry is.
-__device__ __noinline__ double exact_squares(uint4 raw) {
-  float x[8];
-  unpack8(raw, x);
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
-  return sum;
-}
-
-// Whether one of the warp's rows may hold an infinity or a NaN (or its finite
-// squares add up to 2^255 and more): its sum is to be taken of exact_squares.
-__device__ __forceinline__ bool any_huge(double sum) {
-  return __any_sync(0xffffffffu, __double2hiint(sum) >= (1023 + 255) << 20);
-}
-
-// fp32(1 / sqrt(mean of a row's squares + eps)), raw the thread's part.
+// fp32(1 / sqrt(mean of a row's squares + eps)), sum the thread's part.
 template <int D>
-__device__ __forceinline__ float inverse_norm(const uint4& raw, double eps) {
-  auto row_sum = [](double sum) {
+__device__ __forceinline__ float inverse_norm(double sum, double eps) {
 #pragma unroll
-    for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-  };
-  double sum = row_sum(squares(raw));
-  if (any_huge(sum)) sum = row_sum(exact_squares(raw));
+  for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return static_cast<float>(rsqrt(sum * (1.0 / D) + eps));
 }
 
@@ -107,17 +87,28 @@ __device__ __forceinline__ float inverse_norm(const uint4& raw, double eps) {
 // one root instead of four.
 template <int D>
 __device__ __forceinline__ float inverse_norm4(const uint4 (&raw)[4], double eps, int sub) {
+  const double q[4] = {squares(raw[0]), squares(raw[1]), squares(raw[2]), squares(raw[3])};
   const bool odd = sub & 1, high = sub & 2;
-  auto row_sum = [&](double q0, double q1, double q2, double q3) {
-    const double a = (odd ? q1 : q0) + __shfl_xor_sync(0xffffffffu, odd ? q0 : q1, 1);
-    const double b = (odd ? q3 : q2) + __shfl_xor_sync(0xffffffffu, odd ? q2 : q3, 1);
-    double sum = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
+  const double a = (odd ? q[1] : q[0]) + __shfl_xor_sync(0xffffffffu, odd ? q[0] : q[1], 1);
+  const double b = (odd ? q[3] : q[2]) + __shfl_xor_sync(0xffffffffu, odd ? q[2] : q[3], 1);
+  double sum = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
 #pragma unroll
-    for (int o = D / 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-  };
-  double sum = row_sum(squares(raw[0]), squares(raw[1]), squares(raw[2]), squares(raw[3]));
-  if (any_huge(sum)) sum = row_sum(exact_squares(raw[0]), exact_squares(raw[1]), exact_squares(raw[2]), exact_squares(raw[3]));
+  for (int o = D / 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return static_cast<float>(rsqrt(sum * (1.0 / D) + eps));
+}
+
+// A row with an infinity or a NaN (or finite squares of 2^255 and more together)
+// has an inverse norm below this, and is taken of converted numbers: infinite or
+// NaN where an entry is.
+constexpr float kTinyNorm = 0x1p-120f;
+template <int D>
+__device__ __noinline__ float exact_norm(const __nv_bfloat16* row, double eps) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < D; ++i) {
+    const double x = __bfloat162float(row[i]);
+    sum = fma(x, x, sum);
+  }
   return static_cast<float>(rsqrt(sum * (1.0 / D) + eps));
 }
 
@@ -185,7 +176,13 @@ __device__ __forceinline__ void rotate_item(const RotateParams& p, uint32_t item
   Turn<PAIRS> turn;
   if (active) load_turn<PAIRS>(p.rot, sc.start + t, sub, turn);
   float norms = 1.f;
-  if (p.rot.q_weight || p.rot.k_weight) norms = inverse_norm4<D>(raw, p.rot.eps, sub);
+  if (p.rot.q_weight || p.rot.k_weight) {
+    norms = inverse_norm4<D>(raw, p.rot.eps, sub);
+    const int h = h0 + sub % 4;  // the row
+    if (active && h < heads && norms < kTinyNorm)
+      norms = exact_norm<D>(h < p.H ? row_at(p.q, b, t, h) : row_at(p.k, b, t, h - p.H), p.rot.eps);
+    __syncwarp();  // rows are written, perhaps in place, after all of them have been read
+  }
   const size_t token = static_cast<size_t>(b) * p.chunk.T + t;
 #pragma unroll
   for (int i = 0; i < kHeadsPerItem; ++i) {
@@ -337,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppe
         load_turn<PAIRS>(rot, pos, sub, turn);
       }
       float x[8];
-      const float inv_norm = w ? inverse_norm<D>(k_raw, rot.eps) : 1.f;
+      float inv_norm = w ? inverse_norm<D>(squares(k_raw), rot.eps) : 1.f;
+      if (here && inv_norm < kTinyNorm) inv_norm = exact_norm<D>(row_at(p.k, b, pos - start, h), rot.eps);
       weigh_rotate<D, PAIRS>(rot, w, inv_norm, turn, sub, k_raw, x);
       uint8_t* rec = here ? record_at<KIND, D>(cell, pos) : nullptr;
       if (!rec) continue;
@@ -378,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppe
         load_turn<PAIRS>(rot, pos, sub, turn);
       }
       float x[8];
-      const float inv_norm = w ? inverse_norm<D>(k_raw, rot.eps) : 1.f;
+      float inv_norm = w ? inverse_norm<D>(squares(k_raw), rot.eps) : 1.f;
+      if (here && inv_norm < kTinyNorm) inv_norm = exact_norm<D>(row_at(p.k, b, pos - start, h), rot.eps);
       weigh_rotate<D, PAIRS>(rot, w, inv_norm, turn, sub, k_raw, x);
       // the value row: groups of 32 channels are four neighbouring threads
       float v[8];
@@ -533,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const RopeAppe
           raw = *reinterpret_cast<const uint4*>(row_at(p.k, b, pos - start, h) + 8 * sub);
         }
         float x[8];
-        const float inv_norm = w ? inverse_norm<D>(raw, rot.eps) : 1.f;
+        float inv_norm = w ? inverse_norm<D>(squares(raw), rot.eps) : 1.f;
+        if (here && inv_norm < kTinyNorm) inv_norm = exact_norm<D>(row_at(p.k, b, pos - start, h), rot.eps);
         weigh_rotate<D, PAIRS>(rot, w, inv_norm, turn, sub, raw, x);
         if (here) *reinterpret_cast<uint4*>(res + r * D + 8 * sub) = pack8(x);
       }

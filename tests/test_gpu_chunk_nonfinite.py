@@ -306,3 +306,23 @@ def test_many_values_that_are_not_finite(m, kind, T, every):
     want = m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([n - T]), sm_scale=0.1)
     assert torch.equal(out[..., :32], want[..., :32])
     assert torch.isnan(out[..., 32:]).all() if kind != "bf16" else torch.isposinf(out[..., 32:]).all()
+
+
+@pytest.mark.parametrize("eps", [1e75, 1e300])
+def test_norms_under_a_huge_eps(m, eps):
+    """Every row's norm is as small as that of a row of infinities; rows that are not there are not read."""
+    w = seeded_bf16((64,), 3, 0.2) + 1
+    r = m.Rotary(m.rope_table(50, 64), q_weight=w, k_weight=w, eps=eps)
+    x = seeded_bf16((2, 7, 3, 64), 1, 1e37)
+    lens = [7, 2]
+    out = m.loopkv_norm_rope(r, x[:, :, :1], x[:, :, 1:], ints([3, 40]), ints(lens))
+    kv, table = cell_for(m, "q4", 2, 2, 64, 64, 2)
+    m.loopkv_rope_append(kv, 0, 0, r, None, x[:, :, 1:], x[:, :, 1:], table, ints([3, 40]), ints(lens))
+    with np.errstate(all="ignore"):
+        for b, (s, n) in enumerate([(3, 7), (40, 2)]):
+            for o, i in zip(out, (slice(0, 1), slice(1, 3))):
+                want = CO.norm_rope(host(x[b, :n, i]), s + np.arange(n), host(r.table), weight=host(w), eps=eps)
+                assert np.array_equal(host(o[b, :n]), want) and not o[b, n:].any()
+                if i.start:
+                    got = kv.residuals[0][b, :, s % 32: s % 32 + n].transpose(0, 1)
+                    assert np.array_equal(host(got), want)
