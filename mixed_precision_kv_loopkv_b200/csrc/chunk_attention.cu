@@ -1,6 +1,6 @@
 // Attention of a chunk of new tokens over a paged LoopKV cell (sm_100a): the
-// choice between the kernels of chunk_tensor.cuh (128 rows and more of a KV
-// head) and chunk_few.cuh (at most 16), and their launches.
+// choice between the kernels of chunk_few.cuh (at most 16 rows of a KV head, 4-bit
+// and 2-bit cells) and chunk_tensor.cuh (everything else), and their launches.
 #include <mutex>
 
 #include "chunk_few.cuh"
@@ -147,10 +147,13 @@ cudaError_t few_w(const ChunkAttnParams& p, int64_t units, int64_t groups, int d
 // SM with twelve warps at work takes a 32-token group (440 cycles): what the
 // busiest SM has to read, or six for each group that a warp takes one after
 // another; and for each wave of CTAs their start and end, 25, or 45 as clusters.
-// Measured, 512 (sequence, head) pairs of 4100 tokens: CTAs of 12 warps 144 us,
-// of 6 warps 130, of 3 warps 122 (one wave), of 3 warps in clusters of two 131.
-// 16 pairs of 16384 tokens: 12 warps alone 118 us, in clusters of four 38, of
-// eight (which do not all run at once) 50; 16 pairs of 1024: alone 16, four 12.
+// Measured with heads of 128 and 4 bits, 512 (sequence, head) pairs of 4100 tokens:
+// CTAs of 12 warps 151 us, of 6 warps 135, of 3 warps 126 (one wave), of 3 warps in
+// clusters of two 136.  16 pairs of 16384: 12 warps alone 122 us, in clusters of
+// four 40 (taken), of eight (which do not all run at once) 52, 6 warps in clusters
+// of eight 39; 16 pairs of 1024: 14 taken, 12 the best.  With heads of 64 and 2
+// bits, half the work a group, the same choices: 512 pairs of 4100 78 us (the
+// best), 128 pairs 25 (the best), 16 pairs of 16384 27 (best 25), of 1024 9.0 (8.4).
 template <int KIND, int D>
 cudaError_t launch_few(const ChunkAttnParams& p, cudaStream_t stream) {
   const int dev = current_device();

@@ -10,10 +10,11 @@
 // shared memory at the end.
 //
 // Measured on a B200, four tokens of 32 sequences over 4096 4-bit tokens and 16
-// heads of 128 (337 MB): 122 us, 2.8 TB/s, 42 % of measured; the 128-row kernel
-// 311 us.  Bound by instruction issue and its latencies (1035 a group, half of
+// heads of 128 (337 MB): 126 us, 2.7 TB/s, 41 % of measured; the 128-row kernel
+// 311 us.  Bound by instruction issue and its latencies (1000 a group, half of
 // the issue slots used with 12 warps an SM: the outputs and queries alone are 96
-// registers); 16 warps with the queries in shared memory spill: 10 % slower.
+// registers, and 4 bytes a thread are spilled for heads of 128); 16 warps with the
+// queries in shared memory spill more: 10 % slower.
 //
 // Operand layout.  A product's columns (keys, or channels) are the eight
 // thread quads, its depth two pairs for each thread r of a quad.

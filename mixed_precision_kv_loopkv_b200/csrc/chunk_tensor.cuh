@@ -4,7 +4,8 @@
 // heads that share the KV head), over the keys j that it sees,
 //   out_i = sum_j 2^(s_ij - m_i) v_j / sum_j 2^(s_ij - m_i),
 //   s_ij = sm_scale log2(e) q_i . k_j,
-// with a reference m_i that follows the running maximum.  Both products are
+// with a reference m_i that follows the running maximum.  At most 16 rows of 4-bit
+// and 2-bit cells go to chunk_few.cuh, all else comes here.  Both products are
 // 128 x N x 16 fp16 ones with fp32 sums in tensor memory.  fp16 and not bf16:
 // with 8 bits the rounding of dequantised keys alone moved the weights by half a
 // percent where channels stick out; powers of two a block keep it in range.
@@ -18,10 +19,12 @@
 // split the context over a cluster and join through its shared memory.
 //
 // Measured on a B200 (device time), 16 heads of 128 over 4-bit cells: 2048
-// tokens at 16384: 377 us, 685 TFLOP/s, 42 % of measured; 4 x up to 512 tokens
+// tokens at 16384: 371 us, 695 TFLOP/s, 42 % of measured; 4 x up to 512 tokens
 // beside 2048 stored: 67 us; bf16 cells, 6 x up to 301 tokens, 16 heads on 4 KV
-// heads, context up to 1801: 59 us.  Bound by the softmax warps' latency (issue
-// 55 % busy, tensor pipe 38 %, exp unit 30 %; without dequantising 348 us, without exponentials 332 us).
+// heads, context up to 1801: 58 us.  Bound by the softmax warps' latency (issue
+// 60 % busy, tensor pipe 38 %, exp unit 31 %).  With 256 rows the compiler spills
+// 16 to 28 bytes a thread.  The end of the kernel works its place out anew: what
+// it needs, held over the steps, cost 395 us.
 // Steps of 128 keys that reuse their logits' columns for the weights: 428-490 us
 // (each product waits for the softmax); 16 dequantising warps of 56 registers:
 // 510 us (spills); bf16x2-free softmax in scalar operations: 3 % slower.
@@ -43,8 +46,8 @@ constexpr int kPolyPair = 3;                         // of four pairs of weights
 // A block's keys (values) are stored as x 2^-e with e such that the largest is
 // in [2^-7, 2^-6): then 2^24 times a 4-bit scale, at most 2^24 2 2^-6 / 15 <
 // 35000 (2^22 times a 2-bit one: 2^22 2 2^-6 / 3 < 43700), is a finite fp16
-// number, and the code itself, read as a subnormal fp16 number (code 2^-24; 2-bit
-// codes stand two bits higher), needs no conversion.
+// number (rounded to 16 bits as well), and the code itself, read as a subnormal
+// fp16 number (code 2^-24; 2-bit codes stand two bits higher), needs no conversion.
 constexpr int kTopExp = -6;
 
 // The outputs of a row are held in units of 2^(m + v): m is the reference of its

@@ -18,12 +18,12 @@
 //   norms and rotation of 3 x up to 2731 tokens, 32 + 8 heads of 64, rotation of
 //   32: 20.5 us, 3.4 TB/s of 70 MB; instruction issue (27 a value)
 //   64 sequences x 1 token, 16 + 16 heads of 128: 3.6 us; one pass' latency
-//   append of 8191 tokens, 16 heads of 128, 4-bit, queries rotated: 59 us for
+//   append of 8191 tokens, 16 heads of 128, 4-bit, queries rotated: 60 us for
 //   155 MB; instruction issue (the quantiser and the rotation); with 64
 //   registers and eight CTAs an SM (72 and seven: 60 us; rows unrolled four
 //   times, 94 registers: 91 us, the code outgrows the instruction cache); heads
 //   of 128 spill 8 to 12 bytes a thread
-//   append of 64 x 1 token: 8.0 us, five dependent round trips
+//   append of 64 x 1 token: 8.7 us, five dependent round trips
 #include "append_ops.cuh"
 #include "chunk_common.cuh"
 
