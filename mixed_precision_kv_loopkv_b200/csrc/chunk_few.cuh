@@ -241,9 +241,8 @@ struct FewWarp {
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float t = top[i] < INFINITY ? top[i] : NAN;    // +inf: its weight is inf - inf
-        const float m_new = t <= m_ref[i] + kLogitAbove ? m_ref[i] : t;
-        const float v_new = value_ref(v_ref[i], m_ref[i], m_new, t - m_new + value_exp);
+        const float m_new = logit_ref(m_ref[i], top[i]);
+        const float v_new = value_ref(v_ref[i], m_ref[i], m_new, top[i] - m_new + value_exp);
         const float shrink = m_new == m_ref[i] ? 0.f : m_ref[i] - m_new, g = fast_exp2(shrink + (v_ref[i] - v_new));
         sum[i] *= fast_exp2(shrink);
         m_ref[i] = m_new;

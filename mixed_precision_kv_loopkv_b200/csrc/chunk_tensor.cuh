@@ -69,6 +69,13 @@ constexpr float kLogitAbove = 8.f, kMostAbove = 12.f;  // what is not above m, v
 __device__ __forceinline__ bool refs_move(float m, float v, float top, float most) {
   return !(top <= m + kLogitAbove) || most > m + v + kMostAbove;
 }
+// m of a row after new logits of which `top` is the largest.  A NaN among them, or
+// +inf, whose weight is inf - inf, is the row's reference from then on: the
+// weights, the sum and with them all of the row are NaN.
+__device__ __forceinline__ float logit_ref(float m, float top) {
+  top = top < INFINITY ? top : NAN;
+  return top > m + kLogitAbove || top != top ? top : m;
+}
 // v of a row whose reference moved from m to m_new and whose largest new
 // contribution is 2^(m_new + most).  Rounded so that 2^(m + v) of what is there
 // never grows by itself.
@@ -1008,14 +1015,11 @@ __global__ void __launch_bounds__(chunk_threads<MT>(), 1) chunk_tensor_kernel(co
         a = max_nan(max3_nan(a, __uint_as_float(x[14]), __uint_as_float(x[15])), b);
         block_top[c] = a * f[c];
       }
-      float top = max_nan(max3_nan(block_top[0], block_top[1], block_top[2]), block_top[3]);
+      const float top = max_nan(max3_nan(block_top[0], block_top[1], block_top[2]), block_top[3]);
       const float most = fmaxf(max3(block_top[0] + vexp[0], block_top[1] + vexp[1], block_top[2] + vexp[2]), block_top[3] + vexp[3]);
       // The references follow only what is far above them: O is rescaled rarely.
       if (__any_sync(0xffffffffu, refs_move(m_ref, v_ref, top, most))) {
-        // a NaN among the logits, or +inf, whose weight is inf - inf, is the row's
-        // reference: the weights, the sum and with them all of the row are NaN
-        top = top < INFINITY ? top : NAN;
-        const float m_new = top <= m_ref + kLogitAbove ? m_ref : top;
+        const float m_new = logit_ref(m_ref, top);
         float above = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c) above = fmaxf(above, block_top[c] - m_new + vexp[c]);

@@ -20,7 +20,7 @@
 //   64 sequences x 1 token, 16 + 16 heads of 128: 3.6 us; one pass' latency
 //   append of 8191 tokens, 16 heads of 128, 4-bit, queries rotated: 60 us for
 //   155 MB; instruction issue (the quantiser and the rotation); with 64
-//   registers and eight CTAs an SM (72 and seven: 60 us; rows unrolled four
+//   registers and eight CTAs an SM (72 and seven: 1 us more; rows unrolled four
 //   times, 94 registers: 91 us, the code outgrows the instruction cache); heads
 //   of 128 spill 8 to 12 bytes a thread
 //   append of 64 x 1 token: 8.7 us, five dependent round trips

@@ -326,3 +326,22 @@ def test_norms_under_a_huge_eps(m, eps):
                 if i.start:
                     got = kv.residuals[0][b, :, s % 32: s % 32 + n].transpose(0, 1)
                     assert np.array_equal(host(got), want)
+
+
+@pytest.mark.parametrize("kind,T,start,current", [("q4", 150, 1500, True), ("bf16", 150, 1500, False), ("bf16", 300, 20, True),
+                                                  ("q4", 8, 1500, False), ("q2", 8, 1500, False), ("q4", 3, 1503, False)])
+def test_a_nan_stays_where_nothing_follows(m, kind, T, start, current):
+    """A row that sees a NaN logit and after it only keys that it masks is NaN,
+    however the context is split over CTAs and warps."""
+    B = 3
+    few = T < 16
+    last = (start + T - 1) // 32                                     # the last group, masked for the chunk's first rows
+    at = [32 * (last - back) + 1 if few else start + 5 + 40 * b for b, back in enumerate((3, 6, 12))]
+
+    def spoil(b, q, k, v, n):
+        k[at[b], 0, 9] = INF if few else NAN                          # a full group of a quantised cell goes as a whole
+
+    _, _, _, out = run_case(m, kind, 64, T, start, current, spoil, B=B)
+    for b in range(B):
+        first = 0 if few else at[b] - start
+        assert torch.isnan(out[b, first:]).all() and not torch.isnan(out[b, :first]).any()
