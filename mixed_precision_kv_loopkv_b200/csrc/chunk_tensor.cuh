@@ -90,14 +90,14 @@ struct alignas(16) RowStats {
 };
 
 // The references of several partial results together: m is their largest, m + v the
-// largest unit.  `next` gives them one after another.
+// largest unit, and both NaN where one is.  `next` gives them one after another.
 template <typename Next>
 __device__ __forceinline__ RowStats join_refs(int count, Next&& next) {
   float m = -INFINITY, unit = -INFINITY;
   for (int i = 0; i < count; ++i) {
     const RowStats s = next(i);
-    m = fmaxf(m, s.m);
-    unit = fmaxf(unit, s.m + s.v);
+    m = max_nan(m, s.m);
+    unit = max_nan(unit, s.m == -INFINITY ? -INFINITY : s.m + s.v);
   }
   return RowStats{m, 0.f, unit - m};
 }

@@ -345,3 +345,23 @@ def test_a_nan_stays_where_nothing_follows(m, kind, T, start, current):
     for b in range(B):
         first = 0 if few else at[b] - start
         assert torch.isnan(out[b, first:]).all() and not torch.isnan(out[b, :first]).any()
+
+
+def split_case(m, kind, start, T, heads, spoil):
+    """One sequence's chunk of current rows in a cell whose capacity is far larger: its
+    few keys are met by some warps of some CTAs, the others see none."""
+    k, v, q = seeded_bf16((1, start + T, 1, 64), 1), seeded_bf16((1, start + T, 1, 64), 2), seeded_bf16((1, T, heads, 64), 3, 0.3)
+    spoil(k[0, :, 0], v[0, :, 0])
+    kv, table = cell_for(m, kind, 1, 1, 64, 4000, heads)
+    m.loopkv_rope_append(kv, 0, 0, None, None, k[:, :start], v[:, :start], table, ints([0]))
+    return m.loopkv_chunk_attention(kv, 0, 0, q, table, ints([start]), k_cur=k[:, start:], v_cur=v[:, start:])
+
+
+@pytest.mark.parametrize("kind,start", [("q2", 30), ("q4", 30), ("q2", 62), ("q4", 100), ("q2", 333), ("bf16", 400)])
+@pytest.mark.parametrize("T,heads", [(1, 8), (2, 8), (60, 2)])
+def test_a_nan_key_in_one_part_of_a_split_context(m, kind, start, T, heads):
+    """A part whose rows have no logit but a NaN still counts in the join."""
+    def spoil(k, v):
+        k[start - 1, 5] = NAN                                         # in the open group
+
+    assert torch.isnan(split_case(m, kind, start, T, heads, spoil)).all()
