@@ -101,9 +101,10 @@ __device__ __forceinline__ RowStats join_refs(int count, Next&& next) {
   }
   return RowStats{m, 0.f, unit - m};
 }
-// One of them into sum and outputs; skipped where it saw no key, or none with a weight.
+// One of them into sum and outputs; skipped where it saw no key, or none with a
+// weight.  An output is never given a weight of 0: it may be an infinity.
 __device__ __forceinline__ void join_part(RowStats& all, const RowStats& s, float4& acc, const float4& x) {
-  const float d = s.m - all.m, w = fast_exp2(d + s.v - all.v);
+  const float d = s.m - all.m, w = max_nan(fast_exp2(d + s.v - all.v), 0x1p-126f);
   all.sum = fmaf(fast_exp2(d), s.sum, all.sum);
   acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
 }

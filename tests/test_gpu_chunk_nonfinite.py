@@ -365,3 +365,17 @@ def test_a_nan_key_in_one_part_of_a_split_context(m, kind, start, T, heads):
         k[start - 1, 5] = NAN                                         # in the open group
 
     assert torch.isnan(split_case(m, kind, start, T, heads, spoil)).all()
+
+
+@pytest.mark.parametrize("kind", ["q4", "q2", "bf16"])
+@pytest.mark.parametrize("T,heads", [(1, 8), (2, 8), (60, 2)])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_infinite_values_beside_far_larger_ones(m, kind, T, heads, value):
+    """A part with nothing but infinite values joins parts of values of 2^30: its
+    share of them is not 0 times infinity."""
+    def spoil(k, v):
+        v[:40] *= 2.0**30
+        v[40] = value                                                 # the first current row
+
+    out = split_case(m, kind, 40, T, heads, spoil)
+    assert torch.isnan(out).all() if value != value else (out == value).all()
