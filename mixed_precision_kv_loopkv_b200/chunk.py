@@ -271,7 +271,9 @@ def loopkv_rope_append(kv: KVCells, loop: int, layer: int, rotary, q, k_new, v_n
     and values bf16 [B, T, Hkv, D] to a stored cell at positions start_pos[b] ..
     start_pos[b] + new_lens[b] - 1, and norm and rotate its queries bf16
     [B, T, H, D] (or None) in the same launch; returns q_out (new: zeros where
-    there is no row)."""
+    there is no row).  start_pos is what the cell holds; a 4-bit or 2-bit cell
+    can go back to the last multiple of 32 tokens and no further, so drafted
+    tokens are appended when they are accepted (LoopedChunkStep.store)."""
     dev = _cell_device(kv, loop, layer)
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
         raise ValueError("k_new must be [batch, tokens, heads, head_dim]")
