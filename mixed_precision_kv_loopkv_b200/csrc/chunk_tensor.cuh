@@ -76,12 +76,13 @@ __device__ __forceinline__ float logit_ref(float m, float top) {
   top = top < INFINITY ? top : NAN;
   return top > m + kLogitAbove || top != top ? top : m;
 }
-// v of a row whose reference moved from m to m_new and whose largest new
+// v of a row whose reference moves from m to m_new and whose largest new
 // contribution is 2^(m_new + most).  Rounded so that 2^(m + v) of what is there
-// never grows by itself.
+// never grows by itself; and brought up to the new contribution, since O is
+// rescaled anyway (left 2^12 behind, it would have to follow again soon).
 __device__ __forceinline__ float value_ref(float v, float m, float m_new, float most) {
   if (m_new != m) v = m == -INFINITY ? kNoValueRef : fmaxf(v - ceilf(m_new - m), kNoValueRef);
-  return most > v + kMostAbove ? ceilf(most) : v;
+  return fmaxf(v, ceilf(most));
 }
 
 // A partial result of a row: its outputs are in units of 2^(m + v), its sum of 2^m.
